@@ -22,7 +22,9 @@
  * subm3d_forward_fused with a residual-block epilogue); the backward
  * (subm3d_backward_data, subm3d_backward_weight); the resolution changes
  * (subm3d_expand: subdivide / upsample / channel2spatial; subm3d_pool:
- * downsample max / mean, spatial2channel); diagnostics (subm3d_map_run_layout,
+ * downsample max / mean, spatial2channel); what stands around the convolution in
+ * a trained block (subm3d_layer_norm and its backward, subm3d_rotary,
+ * subm3d_adamw); diagnostics (subm3d_map_run_layout,
  * subm3d_device_status, subm3d_status_string, subm3d_abi_version).
  *
  * Conventions for every entry point:
@@ -397,6 +399,141 @@ SUBM3D_API subm3d_status subm3d_pool(const subm3d_map* fine, const int32_t* coor
                                      subm3d_pool_mode mode, int32_t* out_coords, void* out_feats,
                                      void* workspace, size_t workspace_bytes, int64_t* out_count,
                                      void* stream);
+
+/*
+ * Layer norm over the channels of each row, with an activation:
+ *
+ *   xhat = (x - mean) * rstd,  y = act(xhat * weight + bias),
+ *   mean = sum x / C,  rstd = 1 / sqrt(sum (x - mean)^2 / C + eps)
+ *
+ * (the LayerNorm -> activation that stands before a residual block's
+ * convolution; the pages' "gk32_lnormrow" with an activation).  fp32 arithmetic,
+ * y rounded once.
+ *
+ *   x         (device) [N, C] in dtype, rows x_stride elements apart (>= C).
+ *   weight, bias  (device) [C] in affine_dtype, each may be NULL (1 and 0).
+ *             affine_dtype is SUBM3D_F32 or dtype.
+ *   y         (device) [N, C] contiguous, in dtype.  It may be x itself when
+ *             x_stride = C; any other overlap is SUBM3D_E_INVALID.
+ *   mean, rstd  (device) fp32 [N], for the backward; both or neither (NULL).
+ *   act       SUBM3D_ACT_*; eps >= 0.
+ *
+ * All pointers aligned to their element; 16-byte aligned rows run faster.
+ * C <= 2^24, else SUBM3D_E_UNSUPPORTED.  Asynchronous.
+ */
+SUBM3D_API subm3d_status subm3d_layer_norm(const void* x, int64_t n, int32_t channels,
+                                           int64_t x_stride, subm3d_dtype dtype,
+                                           const void* weight, const void* bias,
+                                           subm3d_dtype affine_dtype, float eps, subm3d_act act,
+                                           void* y, float* mean, float* rstd, void* stream);
+
+/*
+ * Its backward.  With dz = dy * act'(xhat * weight + bias) and g = dz * weight:
+ *
+ *   dx = rstd * (g - mean(g) - xhat * mean(g * xhat)),
+ *   dweight = sum over rows of dz * xhat,  dbias = sum over rows of dz.
+ *
+ *   dy        (device) [N, C] in dtype, rows dy_stride elements apart (>= C).
+ *   x, weight, bias, act  as given to the forward; mean, rstd as it wrote them.
+ *   dx        (device) [N, C] contiguous in dtype, or NULL when not wanted.
+ *   dweight, dbias  (device) fp32 [C], overwritten; each may be NULL.  The rows
+ *             are summed in a fixed order: the same call gives the same bits.
+ *   workspace (device) >= subm3d_layer_norm_workspace_bytes(N, C) bytes, 16-byte
+ *             aligned, for dweight and dbias (may be NULL when both are).  It
+ *             holds nothing between calls.
+ *
+ * No output may overlap another buffer.  N = 0 writes zeros to dweight and
+ * dbias.  Asynchronous.
+ */
+SUBM3D_API size_t subm3d_layer_norm_workspace_bytes(int64_t n, int32_t channels);
+SUBM3D_API subm3d_status subm3d_layer_norm_backward(
+    const void* dy, int64_t dy_stride, const void* x, int64_t x_stride, int64_t n,
+    int32_t channels, subm3d_dtype dtype, const float* mean, const float* rstd,
+    const void* weight, const void* bias, subm3d_dtype affine_dtype, subm3d_act act, void* dx,
+    float* dweight, float* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Rotary positions with 1 to 4 axes: for voxels, the axes z, y, x of their
+ * coordinates (the pages' rope_phases_from_coords; trellis_sparse_mrp_mlx commit
+ * log: 63 frequencies padded to 64 with 1 + 0j).
+ *
+ * A head vector of head_dim channels is head_dim / 2 pairs.  The first
+ * axis_pairs[0] of them turn with axis 0 of the row's position, the next
+ * axis_pairs[1] with axis 1, ...; pairs behind the last axis' are copied.  Pair j
+ * of an axis with n pairs turns by the angle position * theta^(-j / n):
+ *
+ *   (x0, x1) -> (x0 cos - x1 sin, x0 sin + x1 cos);
+ *
+ * inverse != 0 turns by the opposite angle, which is the gradient of the
+ * forward.  The angle is reduced in fp64, so far positions are exact to fp32.
+ *
+ *   x, y      (device) [N, heads, head_dim] in dtype, the channels contiguous,
+ *             rows and heads x_row / x_head (y_row / y_head) elements apart, so a
+ *             slice of a packed projection is turned where it lies.  y may be x
+ *             with the same strides; any other pair whose first and last bytes
+ *             enclose a common one is SUBM3D_E_INVALID.
+ *   positions (device) [N, axes], int32, or fp32 with positions_f32 != 0; rows
+ *             pos_stride elements apart, e.g. coords + 1 with pos_stride 4.
+ *   axis_pairs (host) [axes], each >= 0, together <= head_dim / 2.
+ *   halves    0: pair p = channels (2p, 2p + 1); 1: (p, p + head_dim / 2).
+ *
+ * head_dim even and <= 512, else SUBM3D_E_UNSUPPORTED.  theta > 0 and finite.
+ * All pointers aligned to their element.  Asynchronous.
+ */
+SUBM3D_API subm3d_status subm3d_rotary(const void* x, int64_t x_row, int64_t x_head, int64_t n,
+                                       int32_t heads, int32_t head_dim, subm3d_dtype dtype,
+                                       const void* positions, int32_t positions_f32,
+                                       int64_t pos_stride, int32_t axes,
+                                       const int32_t* axis_pairs, double theta, int32_t halves,
+                                       int32_t inverse, void* y, int64_t y_row, int64_t y_head,
+                                       void* stream);
+
+/*
+ * One AdamW step (decoupled weight decay) over many tensors:
+ *
+ *   m' = beta1 m + (1 - beta1) g,  v' = beta2 v + (1 - beta2) g^2,
+ *   p' = p (1 - lr wd) - lr / (1 - beta1^t) * m' / (sqrt(v') / sqrt(1 - beta2^t) + eps)
+ *
+ * in fp32.  Moments in 32 bits (state_bits 32): exp_avg = m and exp_avg_sq = v,
+ * fp32.  In 8 bits: exp_avg = m and exp_avg_sq = sqrt(v) as e4m3 bytes, each 32
+ * consecutive elements with one E8M0 scale byte (the value 2^(byte - 127); the
+ * smallest power of two for which the largest magnitude is <= 448 times it; 255 =
+ * NaN when the 32 hold an infinity or a NaN), rounded stochastically with random
+ * bits hashed from (seed, t, the tensor's number in the call, the element); a
+ * positive sqrt(v) is never stored as zero.  Zero bytes are the zero state.
+ *
+ * subm3d_adamw_tensor: param (param_dtype), grad (grad_dtype), the moments, the
+ * scale bytes [ceil(n / 32)] (8 bits only), master = fp32 master weights or NULL
+ * (with one, the step is taken on it and param receives its rounding; param's own
+ * value is not read), n elements, all contiguous (device) and aligned to their
+ * element.  subm3d_adamw_step: step = t >= 1, or step_device (device int32) when
+ * not NULL; lr, or lr_device (device fp32) when not NULL: what a captured graph
+ * replays with new values.
+ *
+ * Buffers that are written may not overlap anything else in the call, else
+ * SUBM3D_E_INVALID.  Asynchronous; `tensors` and `step` (host) are read before
+ * the call returns.
+ */
+typedef struct {
+  void* param;
+  const void* grad;
+  void* exp_avg;
+  void* exp_avg_sq;
+  void* exp_avg_scale;
+  void* exp_avg_sq_scale;
+  void* master;
+  int64_t n;
+} subm3d_adamw_tensor;
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;
+  const int32_t* step_device;
+  const float* lr_device;
+  int32_t param_dtype, grad_dtype, state_bits;
+  uint32_t seed;
+} subm3d_adamw_step;
+SUBM3D_API subm3d_status subm3d_adamw(const subm3d_adamw_tensor* tensors, int32_t count,
+                                      const subm3d_adamw_step* step, void* stream);
 
 /*
  * Device pointers into the map's x-run layout, for tests and tools: the

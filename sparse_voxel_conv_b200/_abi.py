@@ -84,6 +84,16 @@ def _load() -> ctypes.CDLL:
                                        ctypes.POINTER(i64), vp]),
         "subm3d_backward_weight": (ctypes.c_int, [vp, vp, vp, vp, i32, i32, ctypes.c_int, i32,
                                                   vp]),
+        "subm3d_layer_norm": (ctypes.c_int, [vp, i64, i32, i64, ctypes.c_int, vp, vp,
+                                             ctypes.c_int, ctypes.c_float, ctypes.c_int, vp, vp,
+                                             vp, vp]),
+        "subm3d_layer_norm_workspace_bytes": (sz, [i64, i32]),
+        "subm3d_layer_norm_backward": (ctypes.c_int, [vp, i64, vp, i64, i64, i32, ctypes.c_int,
+                                                      vp, vp, vp, vp, ctypes.c_int, ctypes.c_int,
+                                                      vp, vp, vp, vp, sz, vp]),
+        "subm3d_rotary": (ctypes.c_int, [vp, i64, i64, i64, i32, i32, ctypes.c_int, vp, i32, i64,
+                                         i32, vp, ctypes.c_double, i32, i32, vp, i64, i64, vp]),
+        "subm3d_adamw": (ctypes.c_int, [vp, i32, vp, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -269,6 +279,68 @@ def subm3d_pool(handle: MapHandle, coords, feats, channels: int, dtype: int, mod
                          int(workspace_bytes), ctypes.byref(count), _stream(stream))
     _check(st, "subm3d_pool")
     return int(count.value)
+
+
+def subm3d_layer_norm(x, n: int, channels: int, x_stride: int, dtype: int, weight, bias,
+                      affine_dtype: int, eps: float, act: int, y, mean, rstd,
+                      stream=None) -> None:
+    """Enqueue y = act(layer norm of x's rows); raises Subm3dError on an argument error."""
+    st = lib.subm3d_layer_norm(_ptr(x), n, channels, x_stride, dtype, _ptr(weight), _ptr(bias),
+                               affine_dtype, eps, act, _ptr(y), _ptr(mean), _ptr(rstd),
+                               _stream(stream))
+    _check(st, "subm3d_layer_norm")
+
+
+def subm3d_layer_norm_workspace_bytes(n: int, channels: int) -> int:
+    return int(lib.subm3d_layer_norm_workspace_bytes(int(n), int(channels)))
+
+
+def subm3d_layer_norm_backward(dy, dy_stride: int, x, x_stride: int, n: int, channels: int,
+                               dtype: int, mean, rstd, weight, bias, affine_dtype: int, act: int,
+                               dx, dweight, dbias, workspace, workspace_bytes: int,
+                               stream=None) -> None:
+    """Enqueue the layer norm's gradients (dx, dweight, dbias may each be None)."""
+    st = lib.subm3d_layer_norm_backward(_ptr(dy), dy_stride, _ptr(x), x_stride, n, channels,
+                                        dtype, _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(bias),
+                                        affine_dtype, act, _ptr(dx), _ptr(dweight), _ptr(dbias),
+                                        _ptr(workspace), workspace_bytes, _stream(stream))
+    _check(st, "subm3d_layer_norm_backward")
+
+
+def subm3d_rotary(x, x_row: int, x_head: int, n: int, heads: int, head_dim: int, dtype: int,
+                  positions, positions_f32: bool, pos_stride: int, axis_pairs, theta: float,
+                  halves: bool, inverse: bool, y, y_row: int, y_head: int, stream=None) -> None:
+    """Enqueue y = x turned by its rows' positions (axis_pairs: pairs per axis)."""
+    pairs = (ctypes.c_int32 * len(axis_pairs))(*axis_pairs)
+    st = lib.subm3d_rotary(_ptr(x), x_row, x_head, n, heads, head_dim, dtype, _ptr(positions),
+                           1 if positions_f32 else 0, pos_stride, len(axis_pairs), pairs, theta,
+                           1 if halves else 0, 1 if inverse else 0, _ptr(y), y_row, y_head,
+                           _stream(stream))
+    _check(st, "subm3d_rotary")
+
+
+class AdamWTensor(ctypes.Structure):
+    """subm3d_adamw_tensor: device addresses of one tensor's buffers (0 = none)."""
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p),
+                ("exp_avg_scale", ctypes.c_void_p), ("exp_avg_sq_scale", ctypes.c_void_p),
+                ("master", ctypes.c_void_p), ("n", ctypes.c_int64)]
+
+
+class AdamWStep(ctypes.Structure):
+    """subm3d_adamw_step: one step's numbers."""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("step", ctypes.c_int64), ("step_device", ctypes.c_void_p),
+                ("lr_device", ctypes.c_void_p), ("param_dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("state_bits", ctypes.c_int32),
+                ("seed", ctypes.c_uint32)]
+
+
+def subm3d_adamw(tensors, count: int, step: AdamWStep, stream=None) -> None:
+    """Enqueue one step over `count` tensors (an array of AdamWTensor)."""
+    st = lib.subm3d_adamw(tensors, int(count), ctypes.byref(step), _stream(stream))
+    _check(st, "subm3d_adamw")
 
 
 def subm3d_map_run_layout(handle: MapHandle):

@@ -243,4 +243,90 @@ cudaError_t launch_pool(const MapLayout& map_lay, const void* map_ws, int32_t gr
                         void* out_feats, void* workspace, int64_t* out_count,
                         cudaStream_t stream);
 
+// Layer norm over C channels of each row (layer_norm.cu).  Row strides are in
+// elements; y is contiguous.  weight / bias may be null; mean and rstd (fp32 [N])
+// are written where given.  y may be x itself when x is contiguous.
+struct LayerNormArgs {
+  const void* x = nullptr;
+  const void* weight = nullptr;
+  const void* bias = nullptr;
+  void* y = nullptr;
+  float* mean = nullptr;
+  float* rstd = nullptr;
+  int64_t n = 0, x_stride = 0;
+  int32_t c = 0, act = 0;
+  float eps = 0.0f;
+  bool bf16 = false, affine_bf16 = false;
+};
+cudaError_t launch_layer_norm(const LayerNormArgs& a, int num_sms, cudaStream_t stream);
+
+// Its backward: dx (null: not wanted) in the features' type, dweight and dbias
+// (each may be null) in fp32 through `partial`: fp32 [layer_norm_chunks][2][C].
+struct LayerNormGradArgs {
+  const void* dy = nullptr;
+  const void* x = nullptr;
+  const float* mean = nullptr;
+  const float* rstd = nullptr;
+  const void* weight = nullptr;
+  const void* bias = nullptr;
+  void* dx = nullptr;
+  float* dweight = nullptr;
+  float* dbias = nullptr;
+  float* partial = nullptr;
+  int64_t n = 0, x_stride = 0, dy_stride = 0;
+  int32_t c = 0, act = 0;
+  bool bf16 = false, affine_bf16 = false;
+};
+int64_t layer_norm_chunks(int64_t n);
+cudaError_t launch_layer_norm_grad(const LayerNormGradArgs& a, int num_sms, cudaStream_t stream);
+
+// Rotary positions (rotary.cu).  Strides in elements; turns[p] = the turns per
+// unit of position of pair p; pairs behind the axes' are copied.
+constexpr int kRotaryMaxAxes = 4;
+constexpr int kRotaryMaxPairs = 256;
+struct RotaryArgs {
+  const void* x = nullptr;
+  void* y = nullptr;
+  const void* pos = nullptr;
+  int64_t n = 0, x_row = 0, x_head = 0, y_row = 0, y_head = 0, pos_stride = 0;
+  int32_t heads = 0, head_dim = 0, axes = 0, pairs = 0;  // pairs: of all axes
+  int32_t axis_pairs[kRotaryMaxAxes] = {};
+  bool bf16 = false, pos_f32 = false, halves = false, inverse = false;
+  double turns[kRotaryMaxPairs] = {};
+};
+cudaError_t launch_rotary(const RotaryArgs& a, int num_sms, cudaStream_t stream);
+
+// AdamW (adamw.cu).  A launch takes up to CAP tensors in its parameters.
+struct AdamWTensor {
+  void* param;
+  const void* grad;
+  void* exp_avg;
+  void* exp_avg_sq;
+  uint8_t* exp_avg_scale;
+  uint8_t* exp_avg_sq_scale;
+  float* master;
+  int64_t n;
+};
+struct AdamWStep {
+  float beta1, one_beta1, beta2, one_beta2, eps;
+  float step_size, inv_sqrt_bc2, decay;        // of the host's step number and rate
+  double lr, weight_decay, log_beta1, log_beta2;  // for the device's
+  int64_t step;
+  const int32_t* step_device;
+  const float* lr_device;
+  uint32_t seed;
+  bool param_bf16, grad_bf16;
+};
+template <int CAP>
+struct AdamWList {
+  AdamWTensor tensors[CAP];
+  uint32_t first_block[CAP];
+  int32_t count, first_tensor;
+};
+constexpr int kAdamWFew = 24, kAdamWMany = 440;
+int64_t adamw_chunk();  // elements a block takes
+template <int CAP>
+cudaError_t launch_adamw(const AdamWStep& a, const AdamWList<CAP>& l, uint32_t blocks, bool bits8,
+                         cudaStream_t stream);
+
 }  // namespace subm3d

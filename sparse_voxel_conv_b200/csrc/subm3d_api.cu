@@ -3,9 +3,13 @@
 // No device memory is allocated here; every buffer belongs to the caller.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <cmath>
 #include <cstdlib>
 #include <cstring>
+#include <memory>
 #include <mutex>
+#include <new>
 
 #include "internal.h"
 #include "subm3d.h"
@@ -437,6 +441,353 @@ subm3d_status subm3d_pool(const subm3d_map* fine, const int32_t* coords, const v
       dtype == SUBM3D_BF16, static_cast<int>(mode), out_coords, out_feats, workspace, out_count,
       static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SUBM3D_OK : SUBM3D_E_CUDA;
+}
+
+namespace {
+
+bool valid_dtype(int d) { return d == SUBM3D_F32 || d == SUBM3D_BF16; }
+bool valid_act(int a) {
+  return a == SUBM3D_ACT_NONE || a == SUBM3D_ACT_GELU || a == SUBM3D_ACT_SILU;
+}
+size_t dtype_bytes(int d) { return d == SUBM3D_BF16 ? 2 : 4; }
+
+constexpr int32_t kMaxNormChannels = 1 << 24;
+constexpr int64_t kMaxElements = int64_t(1) << 46;  // keeps every byte count inside 64 bits
+
+// The SM count of the current device, 0 on error.
+int sm_count() {
+  static std::mutex mu;
+  static int cache[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev >= 0 && dev < 64 && cache[dev] > 0) return cache[dev];
+  int sms = 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev >= 0 && dev < 64) cache[dev] = sms;
+  return sms;
+}
+
+// A buffer of a call: its bytes and whether the call writes it.
+struct Span {
+  uintptr_t begin, end;
+  bool written;
+};
+
+// Whether a written buffer shares a byte with any other one.
+bool clash(Span* spans, size_t count) {
+  std::sort(spans, spans + count,
+            [](const Span& a, const Span& b) { return a.begin < b.begin; });
+  uintptr_t any_end = 0, written_end = 0;
+  for (size_t i = 0; i < count; ++i) {
+    if (spans[i].begin == spans[i].end) continue;
+    if (spans[i].begin < written_end || (spans[i].written && spans[i].begin < any_end))
+      return true;
+    any_end = std::max(any_end, spans[i].end);
+    if (spans[i].written) written_end = std::max(written_end, spans[i].end);
+  }
+  return false;
+}
+Span span(const void* p, int64_t bytes, bool written) {
+  const auto b = reinterpret_cast<uintptr_t>(p);
+  return p ? Span{b, b + static_cast<uintptr_t>(bytes), written} : Span{0, 0, false};
+}
+
+// Bytes from the first element of n rows, `stride` elements apart, to the last.
+int64_t rows_bytes(int64_t n, int64_t stride, int64_t width, size_t esz) {
+  return n > 0 ? ((n - 1) * stride + width) * static_cast<int64_t>(esz) : 0;
+}
+
+subm3d_status of(cudaError_t e) { return e == cudaSuccess ? SUBM3D_OK : SUBM3D_E_CUDA; }
+
+}  // namespace
+
+subm3d_status subm3d_layer_norm(const void* x, int64_t n, int32_t channels, int64_t x_stride,
+                                subm3d_dtype dtype, const void* weight, const void* bias,
+                                subm3d_dtype affine_dtype, float eps, subm3d_act act, void* y,
+                                float* mean, float* rstd, void* stream) {
+  if (n < 0 || channels < 1 || x_stride < channels || !valid_dtype(dtype) || !valid_act(act) ||
+      !valid_dtype(affine_dtype) || (affine_dtype == SUBM3D_BF16 && dtype != SUBM3D_BF16) ||
+      !(eps >= 0.0f) || std::isinf(eps) || !mean != !rstd)
+    return SUBM3D_E_INVALID;
+  if (channels > kMaxNormChannels || (n > 0 && x_stride > kMaxElements / n))
+    return SUBM3D_E_UNSUPPORTED;
+  if (n == 0) return SUBM3D_OK;
+  if (!x || !y) return SUBM3D_E_INVALID;
+  const size_t esz = dtype_bytes(dtype), asz = dtype_bytes(affine_dtype);
+  if (!aligned(x, esz) || !aligned(y, esz) || !aligned(weight, asz) || !aligned(bias, asz) ||
+      !aligned(mean, 4) || !aligned(rstd, 4))
+    return SUBM3D_E_INVALID;
+  const bool in_place = y == x && x_stride == channels;
+  Span spans[] = {span(in_place ? nullptr : x, rows_bytes(n, x_stride, channels, esz), false),
+                  span(weight, channels * static_cast<int64_t>(asz), false),
+                  span(bias, channels * static_cast<int64_t>(asz), false),
+                  span(y, rows_bytes(n, channels, channels, esz), true),
+                  span(mean, 4 * n, true),
+                  span(rstd, 4 * n, true)};
+  if (clash(spans, 6)) return SUBM3D_E_INVALID;
+  subm3d::LayerNormArgs a;
+  a.x = x;
+  a.weight = weight;
+  a.bias = bias;
+  a.y = y;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.n = n;
+  a.x_stride = x_stride;
+  a.c = channels;
+  a.act = act;
+  a.eps = eps;
+  a.bf16 = dtype == SUBM3D_BF16;
+  a.affine_bf16 = affine_dtype == SUBM3D_BF16;
+  const int sms = sm_count();
+  if (sms == 0) return SUBM3D_E_CUDA;
+  return of(subm3d::launch_layer_norm(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+size_t subm3d_layer_norm_workspace_bytes(int64_t n, int32_t channels) {
+  if (n < 0 || channels < 1 || channels > kMaxNormChannels) return 0;
+  return static_cast<size_t>(subm3d::layer_norm_chunks(n)) * 2 * channels * 4;
+}
+
+subm3d_status subm3d_layer_norm_backward(
+    const void* dy, int64_t dy_stride, const void* x, int64_t x_stride, int64_t n,
+    int32_t channels, subm3d_dtype dtype, const float* mean, const float* rstd,
+    const void* weight, const void* bias, subm3d_dtype affine_dtype, subm3d_act act, void* dx,
+    float* dweight, float* dbias, void* workspace, size_t workspace_bytes, void* stream) {
+  if (n < 0 || channels < 1 || x_stride < channels || dy_stride < channels ||
+      !valid_dtype(dtype) || !valid_act(act) || !valid_dtype(affine_dtype) ||
+      (affine_dtype == SUBM3D_BF16 && dtype != SUBM3D_BF16))
+    return SUBM3D_E_INVALID;
+  if (channels > kMaxNormChannels ||
+      (n > 0 && (x_stride > kMaxElements / n || dy_stride > kMaxElements / n)))
+    return SUBM3D_E_UNSUPPORTED;
+  if (!aligned(dweight, 4) || !aligned(dbias, 4)) return SUBM3D_E_INVALID;
+  auto s = static_cast<cudaStream_t>(stream);
+  const int64_t c4 = static_cast<int64_t>(channels) * 4;
+  if (n == 0) {
+    if (dweight && cudaMemsetAsync(dweight, 0, c4, s) != cudaSuccess) return SUBM3D_E_CUDA;
+    if (dbias && cudaMemsetAsync(dbias, 0, c4, s) != cudaSuccess) return SUBM3D_E_CUDA;
+    return SUBM3D_OK;
+  }
+  if (!dx && !dweight && !dbias) return SUBM3D_OK;
+  const bool sums = dweight || dbias;
+  if (!dy || !x || !mean || !rstd || (sums && !workspace)) return SUBM3D_E_INVALID;
+  const size_t need = sums ? subm3d_layer_norm_workspace_bytes(n, channels) : 0;
+  const size_t esz = dtype_bytes(dtype), asz = dtype_bytes(affine_dtype);
+  if (workspace_bytes < need || (sums && !aligned(workspace, 16)) || !aligned(dy, esz) ||
+      !aligned(x, esz) || !aligned(dx, esz) || !aligned(weight, asz) || !aligned(bias, asz) ||
+      !aligned(mean, 4) || !aligned(rstd, 4))
+    return SUBM3D_E_INVALID;
+  Span spans[] = {span(dy, rows_bytes(n, dy_stride, channels, esz), false),
+                  span(x, rows_bytes(n, x_stride, channels, esz), false),
+                  span(mean, 4 * n, false),
+                  span(rstd, 4 * n, false),
+                  span(weight, channels * static_cast<int64_t>(asz), false),
+                  span(bias, channels * static_cast<int64_t>(asz), false),
+                  span(dx, rows_bytes(n, channels, channels, esz), true),
+                  span(dweight, c4, true),
+                  span(dbias, c4, true),
+                  span(sums ? workspace : nullptr, static_cast<int64_t>(need), true)};
+  if (clash(spans, 10)) return SUBM3D_E_INVALID;
+  subm3d::LayerNormGradArgs a;
+  a.dy = dy;
+  a.x = x;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.weight = weight;
+  a.bias = bias;
+  a.dx = dx;
+  a.dweight = dweight;
+  a.dbias = dbias;
+  a.partial = static_cast<float*>(workspace);
+  a.n = n;
+  a.x_stride = x_stride;
+  a.dy_stride = dy_stride;
+  a.c = channels;
+  a.act = act;
+  a.bf16 = dtype == SUBM3D_BF16;
+  a.affine_bf16 = affine_dtype == SUBM3D_BF16;
+  const int sms = sm_count();
+  if (sms == 0) return SUBM3D_E_CUDA;
+  return of(subm3d::launch_layer_norm_grad(a, sms, s));
+}
+
+subm3d_status subm3d_rotary(const void* x, int64_t x_row, int64_t x_head, int64_t n,
+                            int32_t heads, int32_t head_dim, subm3d_dtype dtype,
+                            const void* positions, int32_t positions_f32, int64_t pos_stride,
+                            int32_t axes, const int32_t* axis_pairs, double theta, int32_t halves,
+                            int32_t inverse, void* y, int64_t y_row, int64_t y_head,
+                            void* stream) {
+  if (n < 0 || heads < 0 || head_dim < 2 || !valid_dtype(dtype) || axes < 1 ||
+      axes > subm3d::kRotaryMaxAxes || !axis_pairs || !(theta > 0.0) || std::isinf(theta) ||
+      x_row < 0 || x_head < 0 || y_row < 0 || y_head < 0 || pos_stride < 0)
+    return SUBM3D_E_INVALID;
+  if (head_dim % 2 != 0 || head_dim / 2 > subm3d::kRotaryMaxPairs) return SUBM3D_E_UNSUPPORTED;
+  subm3d::RotaryArgs a;
+  int64_t used = 0;
+  for (int i = 0; i < axes; ++i) {
+    if (axis_pairs[i] < 0 || axis_pairs[i] > head_dim / 2 - used) return SUBM3D_E_INVALID;
+    a.axis_pairs[i] = axis_pairs[i];
+    for (int j = 0; j < axis_pairs[i]; ++j)
+      a.turns[used + j] = std::exp(-std::log(theta) * j / axis_pairs[i]) / 6.283185307179586476925;
+    used += axis_pairs[i];
+  }
+  if (n == 0 || heads == 0) return SUBM3D_OK;
+  // rows and heads of y apart from each other (a row may hold its heads, or a head its rows)
+  if ((heads > 1 && y_head < head_dim) || (n > 1 && y_row < head_dim)) return SUBM3D_E_INVALID;
+  if (n > 1 && heads > 1 &&
+      !(y_row >= (heads - 1) * y_head + head_dim || y_head >= (n - 1) * y_row + head_dim))
+    return SUBM3D_E_INVALID;
+  const int64_t most = kMaxElements / n / heads;
+  if (x_row > most || x_head > most || y_row > most || y_head > most || pos_stride > most)
+    return SUBM3D_E_UNSUPPORTED;
+  const size_t esz = dtype_bytes(dtype);
+  if (!x || !y || !positions || !aligned(x, esz) || !aligned(y, esz) || !aligned(positions, 4))
+    return SUBM3D_E_INVALID;
+  const bool in_place = y == x && (n == 1 || y_row == x_row) && (heads == 1 || y_head == x_head);
+  const auto reach = [&](int64_t row, int64_t head, int64_t width, size_t size) {
+    return ((n - 1) * row + (heads - 1) * head + width) * static_cast<int64_t>(size);
+  };
+  Span spans[] = {span(in_place ? nullptr : x, reach(x_row, x_head, head_dim, esz), false),
+                  span(positions, ((n - 1) * pos_stride + axes) * 4, false),
+                  span(y, reach(y_row, y_head, head_dim, esz), true)};
+  if (clash(spans, 3)) return SUBM3D_E_INVALID;
+  a.x = x;
+  a.y = y;
+  a.pos = positions;
+  a.n = n;
+  a.x_row = x_row;
+  a.x_head = x_head;
+  a.y_row = y_row;
+  a.y_head = y_head;
+  a.pos_stride = pos_stride;
+  a.heads = heads;
+  a.head_dim = head_dim;
+  a.axes = axes;
+  a.pairs = static_cast<int32_t>(used);
+  a.bf16 = dtype == SUBM3D_BF16;
+  a.pos_f32 = positions_f32 != 0;
+  a.halves = halves != 0;
+  a.inverse = inverse != 0;
+  const int sms = sm_count();
+  if (sms == 0) return SUBM3D_E_CUDA;
+  return of(subm3d::launch_rotary(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C++" {
+namespace {
+
+// Launches over `tensors` in lists of up to CAP.
+template <int CAP>
+cudaError_t adamw_lists(const subm3d_adamw_tensor* tensors, int32_t count,
+                        const subm3d::AdamWStep& a, bool bits8, cudaStream_t stream) {
+  subm3d::AdamWList<CAP> l;
+  l.count = 0;
+  int64_t blocks = 0;
+  const auto flush = [&]() -> cudaError_t {
+    cudaError_t e = cudaSuccess;
+    if (l.count > 0)
+      e = subm3d::launch_adamw(a, l, static_cast<uint32_t>(blocks), bits8, stream);
+    l.count = 0;
+    blocks = 0;
+    return e;
+  };
+  for (int32_t i = 0; i < count; ++i) {
+    const subm3d_adamw_tensor& t = tensors[i];
+    if (t.n == 0) continue;
+    const int64_t need = (t.n + subm3d::adamw_chunk() - 1) / subm3d::adamw_chunk();
+    // a list's tensors are consecutive ones: their numbers count from the first
+    if (l.count > 0 && (l.count == CAP || blocks + need > 0x7FFFFFFFll ||
+                        l.first_tensor + l.count != i)) {
+      const cudaError_t e = flush();
+      if (e != cudaSuccess) return e;
+    }
+    if (l.count == 0) l.first_tensor = i;
+    l.first_block[l.count] = static_cast<uint32_t>(blocks);
+    l.tensors[l.count] = {t.param,
+                          t.grad,
+                          t.exp_avg,
+                          t.exp_avg_sq,
+                          static_cast<uint8_t*>(t.exp_avg_scale),
+                          static_cast<uint8_t*>(t.exp_avg_sq_scale),
+                          static_cast<float*>(t.master),
+                          t.n};
+    ++l.count;
+    blocks += need;
+  }
+  return flush();
+}
+
+}  // namespace
+}  // extern "C++"
+
+subm3d_status subm3d_adamw(const subm3d_adamw_tensor* tensors, int32_t count,
+                           const subm3d_adamw_step* step, void* stream) {
+  if (count < 0 || (count > 0 && !tensors) || !step) return SUBM3D_E_INVALID;
+  const subm3d_adamw_step& c = *step;
+  const auto finite_from_0 = [](double v) { return v >= 0.0 && !std::isinf(v); };
+  if (!valid_dtype(c.param_dtype) || !valid_dtype(c.grad_dtype) ||
+      (c.state_bits != 32 && c.state_bits != 8) || !(c.beta1 >= 0.0 && c.beta1 < 1.0) ||
+      !(c.beta2 >= 0.0 && c.beta2 < 1.0) || !finite_from_0(c.eps) ||
+      !finite_from_0(c.weight_decay) || (!c.lr_device && !finite_from_0(c.lr)) ||
+      (!c.step_device && c.step < 1) || !aligned(c.step_device, 4) || !aligned(c.lr_device, 4))
+    return SUBM3D_E_INVALID;
+  if (count == 0) return SUBM3D_OK;
+  const size_t psz = dtype_bytes(c.param_dtype), gsz = dtype_bytes(c.grad_dtype);
+  const bool bits8 = c.state_bits == 8;
+  const size_t ssz = bits8 ? 1 : 4;
+  constexpr int kSpans = 7;
+  std::unique_ptr<Span[]> spans(new (std::nothrow) Span[static_cast<size_t>(count) * kSpans + 2]);
+  if (!spans) return SUBM3D_E_INVALID;
+  size_t k = 0;
+  spans[k++] = span(c.step_device, 4, false);
+  spans[k++] = span(c.lr_device, 4, false);
+  for (int32_t i = 0; i < count; ++i) {
+    const subm3d_adamw_tensor& t = tensors[i];
+    if (t.n < 0) return SUBM3D_E_INVALID;
+    if (t.n > (int64_t(1) << 40)) return SUBM3D_E_UNSUPPORTED;
+    if (t.n == 0) continue;
+    if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq ||
+        (bits8 && (!t.exp_avg_scale || !t.exp_avg_sq_scale)))
+      return SUBM3D_E_INVALID;
+    if (!aligned(t.param, psz) || !aligned(t.grad, gsz) || !aligned(t.exp_avg, ssz) ||
+        !aligned(t.exp_avg_sq, ssz) || !aligned(t.master, 4))
+      return SUBM3D_E_INVALID;
+    const int64_t blocks32 = bits8 ? (t.n + 31) / 32 : 0;
+    spans[k++] = span(t.param, t.n * static_cast<int64_t>(psz), true);
+    spans[k++] = span(t.grad, t.n * static_cast<int64_t>(gsz), false);
+    spans[k++] = span(t.exp_avg, t.n * static_cast<int64_t>(ssz), true);
+    spans[k++] = span(t.exp_avg_sq, t.n * static_cast<int64_t>(ssz), true);
+    spans[k++] = span(bits8 ? t.exp_avg_scale : nullptr, blocks32, true);
+    spans[k++] = span(bits8 ? t.exp_avg_sq_scale : nullptr, blocks32, true);
+    spans[k++] = span(t.master, t.n * 4, true);
+  }
+  if (clash(spans.get(), k)) return SUBM3D_E_INVALID;
+  subm3d::AdamWStep a = {};
+  a.beta1 = static_cast<float>(c.beta1);
+  a.one_beta1 = static_cast<float>(1.0 - c.beta1);
+  a.beta2 = static_cast<float>(c.beta2);
+  a.one_beta2 = static_cast<float>(1.0 - c.beta2);
+  a.eps = static_cast<float>(c.eps);
+  a.lr = c.lr;
+  a.weight_decay = c.weight_decay;
+  a.log_beta1 = std::log(c.beta1);
+  a.log_beta2 = std::log(c.beta2);
+  a.step = c.step;
+  a.step_device = c.step_device;
+  a.lr_device = c.lr_device;
+  a.seed = c.seed;
+  a.param_bf16 = c.param_dtype == SUBM3D_BF16;
+  a.grad_bf16 = c.grad_dtype == SUBM3D_BF16;
+  const double t = static_cast<double>(c.step);
+  a.step_size = static_cast<float>(c.lr / -std::expm1(t * a.log_beta1));
+  a.inv_sqrt_bc2 = static_cast<float>(1.0 / std::sqrt(-std::expm1(t * a.log_beta2)));
+  a.decay = static_cast<float>(1.0 - c.lr * c.weight_decay);
+  auto s = static_cast<cudaStream_t>(stream);
+  return of(count <= subm3d::kAdamWFew
+                ? adamw_lists<subm3d::kAdamWFew>(tensors, count, a, bits8, s)
+                : adamw_lists<subm3d::kAdamWMany>(tensors, count, a, bits8, s));
 }
 
 subm3d_status subm3d_device_status(void* stream) {

@@ -1,0 +1,207 @@
+"""Layer norm over a voxel's channels, with an activation applied on the way.
+
+The norm -> activation that stands before the convolutions of a residual block
+(the pages' LayerNorm kernel "gk32_lnormrow", lingbot-map README; here with the
+activation fused), its backward pass with the reduction of the weight's
+gradient, and a module over SparseTensor.  All of it runs in libsubm3d.so.
+"""
+from __future__ import annotations
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import _abi
+from ._host import _ACTS, _DTYPES, _new, _on_device, _on_side_stream, _same_device, _written
+
+__all__ = ["layer_norm", "layer_norm_forward", "layer_norm_backward", "LayerNorm"]
+
+
+def _rows(t: torch.Tensor, name: str, dtype=None):
+    """t as rows of its last dimension: (tensor, row stride), a view where it can be."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() == 0 or t.shape[-1] == 0:
+        raise ValueError(f"{name} must have at least one channel")
+    c = t.shape[-1]
+    if t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= c:
+        return t, t.stride(0)
+    return t.contiguous(), c
+
+
+def _affine(t, name: str, x: torch.Tensor):
+    if t is None:
+        return None
+    if t.dtype != torch.float32 and t.dtype != x.dtype:
+        raise ValueError(f"{name} must be float32 or {x.dtype}, got {t.dtype}")
+    if t.dim() != 1 or t.shape[0] != x.shape[-1]:
+        raise ValueError(f"{name} must have shape [{x.shape[-1]}]")
+    return t.contiguous()
+
+
+def _affine_code(weight, bias, x: torch.Tensor) -> int:
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise ValueError("weight and bias must have one dtype")
+    first = weight if weight is not None else bias
+    return _DTYPES[x.dtype if first is None else first.dtype]
+
+
+def _codes(x: torch.Tensor, act):
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    if act not in _ACTS:
+        raise ValueError(f"unknown activation {act!r}")
+    return _DTYPES[x.dtype], _ACTS[act]
+
+
+def _norm(x, weight, bias, eps, act, out, stream, stats: bool):
+    dtype, act_code = _codes(x, act)
+    rows, stride = _rows(x, "x")
+    w, b = _affine(weight, "weight", x), _affine(bias, "bias", x)
+    affine_dtype = _affine_code(w, b, x)
+    dev = x.device
+    _same_device(dev, weight=w, bias=b, out=out)
+    c = x.shape[-1]
+    n = x.numel() // c
+    with _on_device(dev):
+        if out is None:
+            y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        else:
+            if out.shape != x.shape or out.dtype != x.dtype or not out.is_contiguous():
+                raise ValueError(f"out must be a contiguous {x.dtype} tensor of x's shape")
+            y = out
+        mean = rstd = None
+        if stats:
+            mean, rstd = torch.empty((2, n), dtype=torch.float32, device=dev).unbind()
+        if stream is not None:
+            _on_side_stream(stream, _new(rows, x), _new(w, weight), _new(b, bias), _new(y, out),
+                            mean, rstd)
+        _abi.subm3d_layer_norm(rows, n, c, stride, dtype, w, b, affine_dtype, eps, act_code, y,
+                               mean, rstd, stream)
+    if out is not None:
+        _written(out)
+    return y, mean, rstd
+
+
+def layer_norm_forward(x: torch.Tensor, weight: torch.Tensor | None = None,
+                       bias: torch.Tensor | None = None, eps: float = 1e-5,
+                       act: str | None = None, out: torch.Tensor | None = None, stream=None):
+    """(y, mean, rstd): layer_norm() and the row statistics (fp32 [rows]) that
+    layer_norm_backward() takes."""
+    return _norm(x, weight, bias, eps, act, out, stream, True)
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
+                        rstd: torch.Tensor, weight: torch.Tensor | None = None,
+                        bias: torch.Tensor | None = None, act: str | None = None,
+                        wanted=(True, True, True), stream=None):
+    """(dx, dweight, dbias) of layer_norm_forward(x, weight, bias, act=act).
+
+    dy: the gradient of y, x's shape and dtype.  mean, rstd: as the forward
+    returned them.  dx has x's dtype; dweight and dbias are fp32 [C] (the sum runs
+    over all rows, in an order that does not change from call to call).  wanted:
+    which of the three to compute; the others are None, and so are dweight without
+    a weight and dbias without a bias.
+    """
+    dtype, act_code = _codes(x, act)
+    if dy.shape != x.shape:
+        raise ValueError("dy must have x's shape")
+    xr, x_stride = _rows(x, "x")
+    dr, dy_stride = _rows(dy, "dy", x.dtype)
+    w, b = _affine(weight, "weight", x), _affine(bias, "bias", x)
+    affine_dtype = _affine_code(w, b, x)
+    dev = x.device
+    c = x.shape[-1]
+    n = x.numel() // c
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t.dtype != torch.float32 or t.numel() != n:
+            raise ValueError(f"{name} must be float32 with one value a row ({n})")
+    mean_c, rstd_c = mean.contiguous(), rstd.contiguous()
+    _same_device(dev, dy=dr, mean=mean_c, rstd=rstd_c, weight=w, bias=b)
+    with _on_device(dev):
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if wanted[0] else None
+        dw = torch.empty(c, dtype=torch.float32, device=dev) if wanted[1] and w is not None else None
+        db = torch.empty(c, dtype=torch.float32, device=dev) if wanted[2] and b is not None else None
+        ws, ws_bytes = None, 0
+        if dw is not None or db is not None:
+            ws_bytes = _abi.subm3d_layer_norm_workspace_bytes(n, c)
+            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        if stream is not None:
+            _on_side_stream(stream, dx, dw, db, ws, _new(xr, x), _new(dr, dy), _new(w, weight),
+                            _new(b, bias), _new(mean_c, mean), _new(rstd_c, rstd))
+        _abi.subm3d_layer_norm_backward(dr, dy_stride, xr, x_stride, n, c, dtype, mean_c, rstd_c,
+                                        w, b, affine_dtype, act_code, dx, dw, db, ws, ws_bytes,
+                                        stream)
+    return dx, dw, db
+
+
+class _LayerNormFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps, act):
+        y, mean, rstd = _norm(x, weight, bias, eps, act, None, None, True)
+        ctx.save_for_backward(x, weight, bias, mean, rstd)
+        ctx.act = act
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, weight, bias, mean, rstd = ctx.saved_tensors
+        dx, dw, db = layer_norm_backward(dy, x, mean, rstd, weight, bias, ctx.act,
+                                         ctx.needs_input_grad[:3])
+        if dw is not None:
+            dw = dw.to(weight.dtype)
+        if db is not None:
+            db = db.to(bias.dtype)
+        return dx, dw, db, None, None
+
+
+def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
+               bias: torch.Tensor | None = None, eps: float = 1e-5, act: str | None = None,
+               out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y = act((x - mean) / sqrt(var + eps) * weight + bias) over x's last dimension.
+
+    x: [..., C] float32 or bfloat16 (rows of a matrix may be strided); weight, bias:
+    optional [C], float32 or x's dtype.  act: None, "gelu" (exact erf form) or
+    "silu".  fp32 arithmetic; y has x's dtype and is rounded once.  Differentiable
+    in x, weight and bias; out (contiguous, may be x) and stream are for calls that
+    autograd does not record.
+    """
+    if torch.is_grad_enabled() and (x.requires_grad or
+                                    (weight is not None and weight.requires_grad) or
+                                    (bias is not None and bias.requires_grad)):
+        if out is not None or stream is not None:
+            raise ValueError("out and stream are not available where gradients are recorded")
+        return _LayerNormFunction.apply(x, weight, bias, eps, act)
+    return _norm(x, weight, bias, eps, act, out, stream, False)[0]
+
+
+class LayerNorm(torch.nn.Module):
+    """Layer norm over each voxel's channels, then `act` (None, "gelu", "silu").
+
+    affine=True holds a weight (ones) and a bias (zeros) of `dtype`: float32, which
+    serves float32 and bfloat16 features, or bfloat16 for bfloat16 features.
+    Takes and returns a SparseTensor (or a tensor [..., C]).
+    """
+
+    def __init__(self, channels: int, eps: float = 1e-5, act: str | None = None,
+                 affine: bool = True, dtype=torch.float32, device=None):
+        super().__init__()
+        self.channels = channels
+        self.eps = eps
+        self.act = act
+        if affine:
+            self.weight = torch.nn.Parameter(torch.ones(channels, dtype=dtype, device=device),
+                                             requires_grad=False)
+            self.bias = torch.nn.Parameter(torch.zeros(channels, dtype=dtype, device=device),
+                                           requires_grad=False)
+        else:
+            self.weight = self.bias = None
+
+    def forward(self, x):
+        feats = x if isinstance(x, torch.Tensor) else x.feats
+        if feats.shape[-1] != self.channels:
+            raise ValueError(f"x must have {self.channels} channels")
+        y = layer_norm(feats, self.weight, self.bias, self.eps, self.act)
+        return y if isinstance(x, torch.Tensor) else x.replace(y)

@@ -1,0 +1,200 @@
+"""AdamW over many tensors in one launch, with moments in 32 or in 8 bits.
+
+What a training loop does with the gradients of backward_weight() and of the
+autograd functions: one call of libsubm3d.so updates all weights and moments.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _abi
+from ._host import _DTYPES, _on_device, _on_side_stream, _written
+
+__all__ = ["adamw_step", "AdamW"]
+
+_BLOCK = 32  # elements that share a scale of the 8-bit moments
+_CODE, _SCALE = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+def _each(name, tensors, like, dtype, sizes=None):
+    """Checks a list that runs along the parameters: their number, type, device,
+    sizes and layout."""
+    if len(tensors) != len(like):
+        raise ValueError(f"{name} must have one tensor for each of {len(like)} parameters")
+    dev = like[0].device
+    for i, (t, p) in enumerate(zip(tensors, like)):
+        if t.dtype != dtype:
+            raise ValueError(f"{name}[{i}] must be {dtype}, got {t.dtype}")
+        if t.device != dev:
+            raise ValueError(f"{name}[{i}] must be on {dev}, got {t.device}")
+        if t.numel() != (p.numel() if sizes is None else sizes[i]):
+            raise ValueError(f"{name}[{i}] has the wrong number of elements")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}[{i}] must be contiguous")
+
+
+def _scalar(t, name, dtype, dev):
+    if t.numel() != 1 or t.dtype != dtype or t.device != dev:
+        raise ValueError(f"{name} as a tensor must be one {dtype} on {dev}")
+    return t.data_ptr()
+
+
+def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0.9, 0.999),
+               eps: float = 1e-8, weight_decay: float = 0.01, masters=None, exp_avg_scales=None,
+               exp_avg_sq_scales=None, seed: int = 0, stream=None) -> None:
+    """One AdamW step over lists of tensors, in place.
+
+        m = b1 m + (1 - b1) g,   v = b2 v + (1 - b2) g^2
+        p = p (1 - lr wd) - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+
+    params: float32 or bfloat16, all of one dtype; grads: likewise (float32
+    gradients of bfloat16 parameters are what backward_weight() gives).  masters:
+    float32 copies that the step is taken on; params then receive their rounding.
+    32-bit moments: exp_avgs (m) and exp_avg_sqs (v) float32.  8-bit moments:
+    exp_avgs (m) and exp_avg_sqs (sqrt(v)) float8_e4m3fn, with exp_avg_scales and
+    exp_avg_sq_scales, float8_e8m0fnu, one scale for each 32 elements; the value is
+    code * scale, zero bytes are the zero state, and rounding is stochastic with
+    random bits made from (seed, step, place in the list, element).
+    step: t >= 1, an int or a CUDA int32 tensor of one element; lr: a float or a
+    CUDA float32 tensor of one element (tensors: read when the work runs, for a
+    captured graph).  All tensors contiguous and on one device.  A tensor that is
+    written may not share memory with another one.
+    """
+    if len(params) == 0:
+        return
+    dev = params[0].device
+    if not params[0].is_cuda:
+        raise ValueError("params must be CUDA tensors")
+    if len(grads) != len(params):
+        raise ValueError(f"grads must have one tensor for each of {len(params)} parameters")
+    p_type, g_type, s_type = params[0].dtype, grads[0].dtype, None
+    if p_type not in _DTYPES or g_type not in _DTYPES:
+        raise ValueError(f"unsupported dtype {p_type} or {g_type}")
+    if len(exp_avgs) != len(params):
+        raise ValueError(f"exp_avgs must have one tensor for each of {len(params)} parameters")
+    s_type = exp_avgs[0].dtype
+    if s_type not in (torch.float32, _CODE):
+        raise ValueError(f"moments must be float32 or {_CODE}, got {s_type}")
+    bits8 = s_type == _CODE
+    _each("params", params, params, p_type)
+    _each("grads", grads, params, g_type)
+    _each("exp_avgs", exp_avgs, params, s_type)
+    _each("exp_avg_sqs", exp_avg_sqs, params, s_type)
+    if masters is not None:
+        _each("masters", masters, params, torch.float32)
+    if bits8:
+        if exp_avg_scales is None or exp_avg_sq_scales is None:
+            raise ValueError("8-bit moments need exp_avg_scales and exp_avg_sq_scales")
+        blocks = [(p.numel() + _BLOCK - 1) // _BLOCK for p in params]
+        _each("exp_avg_scales", exp_avg_scales, params, _SCALE, blocks)
+        _each("exp_avg_sq_scales", exp_avg_sq_scales, params, _SCALE, blocks)
+    elif exp_avg_scales is not None or exp_avg_sq_scales is not None:
+        raise ValueError("32-bit moments have no scales")
+    c = _abi.AdamWStep(beta1=betas[0], beta2=betas[1], eps=eps, weight_decay=weight_decay,
+                       param_dtype=_DTYPES[p_type], grad_dtype=_DTYPES[g_type],
+                       state_bits=8 if bits8 else 32, seed=seed & 0xFFFFFFFF)
+    if isinstance(step, torch.Tensor):
+        c.step_device = _scalar(step, "step", torch.int32, dev)
+    else:
+        c.step = step
+    if isinstance(lr, torch.Tensor):
+        c.lr_device = _scalar(lr, "lr", torch.float32, dev)
+    else:
+        c.lr = lr
+    count = len(params)
+    at = lambda ts: (None,) * count if ts is None else [t.data_ptr() for t in ts]  # noqa: E731
+    array = (_abi.AdamWTensor * count)(*zip(at(params), at(grads), at(exp_avgs), at(exp_avg_sqs),
+                                            at(exp_avg_scales), at(exp_avg_sq_scales),
+                                            at(masters), [p.numel() for p in params]))
+    with _on_device(dev):
+        if stream is not None:
+            _on_side_stream(stream)
+        _abi.subm3d_adamw(array, count, c, stream)
+    _written(*params, *(masters or ()))
+
+
+class AdamW(torch.optim.Optimizer):
+    """AdamW (decoupled weight decay) on adamw_step().
+
+    state_bits: 32, or 8 for moments in about a byte each (see adamw_step).
+    master_weights: keep float32 masters of bfloat16 parameters in the state;
+    without them a bfloat16 weight loses every change below half its spacing.
+    seed: of the 8-bit rounding.  Parameters and gradients must be contiguous CUDA
+    tensors.  In a captured graph call adamw_step() with a device step instead.
+    """
+
+    def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
+                 weight_decay: float = 0.01, state_bits: int = 32, master_weights: bool = False,
+                 seed: int = 0):
+        if state_bits not in (32, 8):
+            raise ValueError("state_bits must be 32 or 8")
+        if lr < 0 or eps < 0 or weight_decay < 0 or not all(0 <= b < 1 for b in betas):
+            raise ValueError("lr, eps and weight_decay must not be negative, betas in [0, 1)")
+        self.seed = int(seed)
+        super().__init__(params, dict(lr=lr, betas=tuple(betas), eps=eps,
+                                      weight_decay=weight_decay, state_bits=state_bits,
+                                      master_weights=master_weights))
+
+    def _state_of(self, p, group):
+        st = self.state[p]
+        if not st:
+            n = p.numel()
+            st["step"] = 0
+            if group["state_bits"] == 32:
+                for k in ("exp_avg", "exp_avg_sq"):
+                    st[k] = torch.zeros(p.shape, dtype=torch.float32, device=p.device)
+            else:
+                for k in ("exp_avg", "exp_avg_sq"):
+                    st[k] = torch.zeros(p.shape, dtype=torch.uint8, device=p.device).view(_CODE)
+                    st[k + "_scale"] = torch.zeros((n + _BLOCK - 1) // _BLOCK, dtype=torch.uint8,
+                                                   device=p.device).view(_SCALE)
+            if group["master_weights"] and p.dtype != torch.float32:
+                st["master"] = p.detach().float()
+        return st
+
+    @torch.no_grad()
+    def step(self, closure=None):
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        if torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("the step number would be frozen into the graph: capture "
+                               "adamw_step() with a device step")
+        call = 0
+        for group in self.param_groups:
+            sets = {}
+            for p in group["params"]:
+                if p.grad is None:
+                    continue
+                if p.grad.is_sparse:
+                    raise ValueError("gradients must be dense")
+                st = self._state_of(p, group)
+                key = (p.device, p.dtype, p.grad.dtype, "master" in st, st["step"])
+                sets.setdefault(key, []).append((p, st))
+            for key, members in sets.items():
+                params = [p for p, _ in members]
+                states = [st for _, st in members]
+                pick = lambda k: [st[k] for st in states]  # noqa: E731
+                bits8 = group["state_bits"] == 8
+                adamw_step(params, [p.grad for p in params], pick("exp_avg"), pick("exp_avg_sq"),
+                           key[-1] + 1, lr=group["lr"], betas=group["betas"], eps=group["eps"],
+                           weight_decay=group["weight_decay"],
+                           masters=pick("master") if key[3] else None,
+                           exp_avg_scales=pick("exp_avg_scale") if bits8 else None,
+                           exp_avg_sq_scales=pick("exp_avg_sq_scale") if bits8 else None,
+                           seed=self.seed + 0x632BE5A7 * call)
+                for st in states:
+                    st["step"] += 1
+                call += 1
+        return loss
+
+    def load_state_dict(self, state_dict):
+        """As torch.optim.Optimizer, but the moments and masters keep their own types
+        (the base class casts them to the parameter's)."""
+        super().load_state_dict(state_dict)
+        saved = [i for g in state_dict["param_groups"] for i in g["params"]]
+        for i, p in zip(saved, (p for g in self.param_groups for p in g["params"])):
+            for k, v in state_dict["state"].get(i, {}).items():
+                if isinstance(v, torch.Tensor):
+                    self.state[p][k] = v.detach().clone().to(p.device)

@@ -15,53 +15,13 @@ import torch
 
 from . import _abi
 from ._abi import Subm3dError
+from ._host import _ACTS, _DTYPES, _cuda_contig, _new, _on_side_stream
 
 __all__ = ["MapHandle", "build_map", "forward", "backward_data", "backward_weight", "SparseTensor",
            "SubMConv3d", "SubMResBlock3d", "Subm3dError", "subdivide", "upsample",
            "channel2spatial", "spatial2channel", "downsample"]
 
 MapHandle = _abi.MapHandle
-
-_DTYPES = {torch.float32: _abi.SUBM3D_F32, torch.bfloat16: _abi.SUBM3D_BF16}
-_ACTS = {None: _abi.SUBM3D_ACT_NONE, "none": _abi.SUBM3D_ACT_NONE, "gelu": _abi.SUBM3D_ACT_GELU,
-         "silu": _abi.SUBM3D_ACT_SILU}
-
-
-def _cuda_contig(t: torch.Tensor, name: str, dtype=None) -> torch.Tensor:
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    return t.contiguous()
-
-
-def _new(t, orig):
-    """t when this binding made it (an allocation or a contiguous copy), else None."""
-    return None if t is orig else t
-
-
-def _on_side_stream(stream, *made) -> None:
-    """Before a call enqueued on `stream` when that is not torch's current stream.
-
-    This binding allocates outputs and scratch, and makes contiguous copies, on
-    the current stream; the caching allocator hands out memory that is free in
-    that stream's order only.  So the side stream first waits for the work
-    already queued on the current stream, and the tensors made here are
-    recorded as in use by the side stream (their memory is not handed out again
-    before its work has run).  `made`: only tensors created here (None skipped);
-    the caller's own tensors are the caller's to manage."""
-    if stream is None:
-        return
-    side = (stream if isinstance(stream, torch.cuda.Stream)
-            else torch.cuda.ExternalStream(int(stream)))
-    current = torch.cuda.current_stream()
-    if side.cuda_stream == current.cuda_stream:
-        return
-    side.wait_stream(current)
-    for t in made:
-        if t is not None:
-            t.record_stream(side)
-
 
 def build_map(coords: torch.Tensor, grid_dim: int, batch: int = 1, stream=None,
               check: bool = True, nbr: torch.Tensor | None = None,
@@ -319,18 +279,41 @@ class SubMResBlock3d(torch.nn.Module):
 
     Both convolutions share `indice_key`, so the map is built once per
     coordinate set; no separate bias, activation or add kernel runs.
+
+    norm=True is the block with layer norms before its convolutions (which then
+    have no bias of their own), and it trains: its gradients are the library's.
+
+        h   = conv1(act(norm1(x)))
+        out = conv2(act(norm2(h))) + x
+
+    Without recorded gradients the skip add is conv2's epilogue; with them it is
+    an add of its own, after conv2's output has been rounded.
     """
 
     def __init__(self, channels: int, indice_key: str = "subm0", act: str = "silu",
-                 dtype=torch.bfloat16, device=None):
+                 dtype=torch.bfloat16, device=None, norm: bool = False):
         super().__init__()
+        if norm:
+            from .norm import LayerNorm
+            for i in ("1", "2"):
+                setattr(self, "norm" + i, LayerNorm(channels, act=act, device=device))
+                setattr(self, "conv" + i, SubMConv3d(channels, channels, indice_key, dtype=dtype,
+                                                     device=device))
+            return
+        self.norm1 = None
         self.conv1 = SubMConv3d(channels, channels, indice_key, act=act, dtype=dtype,
                                 device=device, bias=True)
         self.conv2 = SubMConv3d(channels, channels, indice_key, act=None, dtype=dtype,
                                 device=device, bias=True)
 
     def forward(self, x: SparseTensor) -> SparseTensor:
-        return self.conv2(self.conv1(x), residual=x.feats)
+        if self.norm1 is None:
+            return self.conv2(self.conv1(x), residual=x.feats)
+        h = self.norm2(self.conv1(self.norm1(x)))
+        if torch.is_grad_enabled() and (h.feats.requires_grad or self.conv2.weight.requires_grad):
+            y = self.conv2(h)
+            return y.replace(y.feats + x.feats)
+        return self.conv2(h, residual=x.feats)
 
 
 # ------------------------------------------------------ resolution changes ----
