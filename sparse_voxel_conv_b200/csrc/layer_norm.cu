@@ -16,10 +16,11 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <type_traits>
+#include <atomic>
 
 #include "epilogue.cuh"
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace subm3d {
 
@@ -231,15 +232,24 @@ __global__ void __launch_bounds__(kThreads) norm_dw_join_kernel(const float* par
 
 // ---------------------------------------------------------------- row kernels ----
 //
-// A team works on one row: 2^k lanes of a warp, or several whole warps.  A lane
-// holds kLane = V x E elements of the row in registers: V loads of E elements,
-// 16-byte loads where the rows allow it and single elements otherwise.  The row is
-// read once; its sums go over the team by shuffles, and between warps through one
-// exchange in shared memory.  Teams walk over the rows with their columns' weights
-// in registers and load the next row before they work on this one.
+// A team works on one row: 2^k lanes of a warp, or several whole warps (WIDE).  A
+// lane holds N = V x E elements of the row: V loads of E elements, as wide as the
+// rows' alignment allows.  The row is read once; its sums go over the team by
+// shuffles, and between warps through one exchange in shared memory.  Teams walk
+// over the rows with their columns' weights in registers.  Each lane copies its
+// own part of the rows ahead into its own shared-memory slots (cp.async, kStages
+// deep): no barrier, and the bytes in flight do not cost registers, which are what
+// limits the warps on an SM.
 
+#ifndef KS
+#define KS 4
+#define KG 3
+#endif
+constexpr int kRowStages = KS, kGradStages = KG;
 constexpr int kMaxRowWarps = 16;  // forward: rows up to 16 * 32 * 16 = 8,192 elements
 constexpr int kMaxGradWarps = 8;  // backward: 4,096
+// Resident threads on an SM that the kernels' register bounds allow.
+constexpr int kRowThreads = 768, kWideRowThreads = 512, kGradThreads = 512;
 
 using f2 = unsigned long long;  // two fp32 values
 __device__ __forceinline__ f2 f2_set(float v) { return f2_pack(v, v); }
@@ -248,84 +258,95 @@ __device__ __forceinline__ float f2_sum(f2 v) {
   f2_unpack(v, a, b);
   return a + b;
 }
+__device__ __forceinline__ f2 bf16_pair(uint32_t w) {
+  return f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint32_t to_bf16_pair(f2 v) {
+  float a, b;
+  f2_unpack(v, a, b);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
 
-// E elements as they lie in memory.  (Coherent loads in volatile asm: they stay
-// behind pdl_wait() and in front of the work on the row before.)
-template <typename T, int E>
-struct Raw;
-template <>
-struct Raw<__nv_bfloat16, 8> {
-  uint32_t w[4];
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "l"(p));
+// One instruction each (no handling of subnormal inputs and results, which the
+// uses below do not need).
+__device__ __forceinline__ float exp2_fast(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float rcp_fast(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ f2 exp2_pair(f2 v) {
+  float a, b;
+  f2_unpack(v, a, b);
+  return f2_pack(exp2_fast(a), exp2_fast(b));
+}
+__device__ __forceinline__ f2 rcp_pair(f2 v) {
+  float a, b;
+  f2_unpack(v, a, b);
+  return f2_pack(rcp_fast(a), rcp_fast(b));
+}
+
+// sigmoid(z) of a pair: 1 / (1 + 2^(-z log2 e)).
+__device__ __forceinline__ f2 sigmoid_pair(f2 z) {
+  return rcp_pair(f2_add(exp2_pair(f2_mul(z, f2_set(-1.4426950408889634f))), f2_set(1.0f)));
+}
+
+// Phi(z) and exp(-z^2 / 2) of a pair: the rational-times-Gaussian form that
+// gelu_erf uses (epilogue.cuh), with the factor 1/2 of Phi in its coefficients.
+__device__ __forceinline__ f2 phi_pair(f2 z, f2& gauss) {
+  const f2 mag = z & 0x7FFFFFFF7FFFFFFFull;
+  const f2 t = rcp_pair(f2_fma(mag, f2_set(0.3275911f * 0.70710678118654752f), f2_set(1.0f)));
+  f2 q = f2_fma(t, f2_set(0.5f * 1.061405429f), f2_set(0.5f * -1.453152027f));
+  q = f2_fma(t, q, f2_set(0.5f * 1.421413741f));
+  q = f2_fma(t, q, f2_set(0.5f * -0.284496736f));
+  q = f2_fma(t, q, f2_set(0.5f * 0.254829592f));
+  gauss = exp2_pair(f2_mul(f2_mul(z, z), f2_set(-0.5f * 1.4426950408889634f)));
+  const f2 tail = f2_mul(f2_mul(t, q), gauss);
+  float z0, z1, t0, t1, u0, u1;
+  f2_unpack(z, z0, z1);
+  f2_unpack(tail, t0, t1);
+  f2_unpack(f2_fma(tail, f2_set(-1.0f), f2_set(1.0f)), u0, u1);
+  return f2_pack(z0 >= 0.0f ? u0 : t0, z1 >= 0.0f ? u1 : t1);
+}
+
+template <int ACT>
+__device__ __forceinline__ f2 act_pair(f2 z) {
+  if (ACT == kActSilu) return f2_mul(z, sigmoid_pair(z));
+  if (ACT == kActGelu) {
+    f2 gauss;
+    return f2_mul(z, phi_pair(z, gauss));
   }
-  __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0u; }
-  __device__ __forceinline__ float at(int i) const {
-    return __uint_as_float(i % 2 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+  return z;
+}
+// act'(z): s (1 + z (1 - s)) = s + (z s) (1 - s); Phi(z) + z phi(z).
+template <int ACT>
+__device__ __forceinline__ f2 slope_pair(f2 z) {
+  if (ACT == kActSilu) {
+    const f2 s = sigmoid_pair(z);
+    return f2_fma(f2_mul(z, s), f2_fma(s, f2_set(-1.0f), f2_set(1.0f)), s);
   }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* v) {
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-      o[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
-  }
-};
-template <>
-struct Raw<float, 4> {
-  float w[4];
-  __device__ __forceinline__ void load(const float* p) {
-    asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(w[0]), "=f"(w[1]), "=f"(w[2]), "=f"(w[3])
-                 : "l"(p));
-  }
-  __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0.0f; }
-  __device__ __forceinline__ float at(int i) const { return w[i]; }
-  static __device__ __forceinline__ void store(float* p, const float* v) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  }
-};
-template <>
-struct Raw<__nv_bfloat16, 1> {
-  uint16_t w;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    asm volatile("ld.global.b16 %0, [%1];" : "=h"(w) : "l"(p));
-  }
-  __device__ __forceinline__ void zero() { w = 0; }
-  __device__ __forceinline__ float at(int) const {
-    return __uint_as_float(static_cast<uint32_t>(w) << 16);
-  }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* v) {
-    *p = __float2bfloat16_rn(v[0]);
-  }
-};
-template <>
-struct Raw<float, 1> {
-  float w;
-  __device__ __forceinline__ void load(const float* p) {
-    asm volatile("ld.global.f32 %0, [%1];" : "=f"(w) : "l"(p));
-  }
-  __device__ __forceinline__ void zero() { w = 0.0f; }
-  __device__ __forceinline__ float at(int) const { return w; }
-  static __device__ __forceinline__ void store(float* p, const float* v) { *p = v[0]; }
-};
+  f2 gauss;
+  const f2 phi = phi_pair(z, gauss);
+  return f2_fma(z, f2_mul(gauss, f2_set(0.39894228040143268f)), phi);
+}
 
 // A thread's place.  `lanes` = threads of a team: a power of two up to 32, or whole
 // warps.  The loop over rows is a warp's: `base` is its first team's row, and rows
 // from a.n on (the last round of teams inside a warp) are computed on zeros and not
 // stored, so that all lanes take part in every shuffle.
 struct Team {
-  int lanes, warps;     // warps: of a team of whole warps, else 1
-  int first, step;      // the lane's vectors: first + k step
-  int warp;             // the warp's number in its team
-  int id;               // the team's number in the block
-  bool leader;          // the team's first lane
+  int lanes, warps;      // warps: of a team of whole warps, else 1
+  int first, step;       // the lane's vectors: first + k step
+  int warp;              // the warp's number in its team
+  int id;                // the team's number in the block
+  bool leader;           // the team's first lane
   int64_t base, stride;  // the loop over rows
-  int sub;              // the team's number in the warp
+  int sub;               // the team's number in the warp
 };
 template <int V, bool WIDE>
 __device__ __forceinline__ Team team_of(int lanes) {
@@ -345,6 +366,108 @@ __device__ __forceinline__ Team team_of(int lanes) {
   return t;
 }
 
+// A lane's parts of the rows ahead.  Parts of 4, 8 or 16 bytes are copied into the
+// lane's own shared-memory slots; single bf16 elements (odd widths) are held in
+// registers, one row ahead.
+template <typename T, int E, int V>
+struct Ahead {
+  static constexpr int kBytes = static_cast<int>(sizeof(T)) * E;
+  static constexpr bool kAsync = kBytes >= 4;
+  static constexpr int N = V * E;
+  uint32_t mine, stage;  // addresses: slot of stage 0, bytes between stages
+  uint32_t held[kAsync ? 1 : V];
+
+  __device__ __forceinline__ void init(uint32_t smem) {
+    mine = smem + threadIdx.x * kBytes;
+    stage = blockDim.x * V * kBytes;
+  }
+  // Starts on row p (zeros where `live` is false and behind the row's end).
+  __device__ __forceinline__ void fetch(int s, const T* p, bool live, const Team& t, int vecs) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int v = t.first + k * t.step;
+      const bool on = live && v < vecs;
+      if constexpr (kAsync) {
+        const uint32_t dst = mine + s * stage + k * blockDim.x * kBytes;
+        const T* src = on ? p + v * E : p;
+        const int bytes = on ? kBytes : 0;
+        if constexpr (kBytes == 16)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                       "r"(bytes)
+                       : "memory");
+        else
+          asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src),
+                       "n"(kBytes), "r"(bytes)
+                       : "memory");
+      } else {
+        uint16_t h = 0;
+        if (on) asm volatile("ld.global.b16 %0, [%1];" : "=h"(h) : "l"(p + v));
+        held[k] = h;
+      }
+    }
+  }
+  __device__ __forceinline__ void read(int s, f2 (&v)[N / 2]) const {
+    uint32_t w[kAsync ? V * kBytes / 4 : V];
+    if constexpr (kAsync) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const uint32_t src = mine + s * stage + k * blockDim.x * kBytes;
+        uint32_t* o = w + k * kBytes / 4;
+        if constexpr (kBytes == 16)
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+                       : "r"(src)
+                       : "memory");
+        else
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(o[0]) : "r"(src) : "memory");
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k) w[k] = held[k];
+    }
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      if constexpr (sizeof(T) == 4)
+        v[i] = f2_pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+      else if constexpr (kAsync)
+        v[i] = bf16_pair(w[i]);
+      else
+        v[i] = f2_pack(__uint_as_float(w[2 * i] << 16), __uint_as_float(w[2 * i + 1] << 16));
+    }
+  }
+};
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
+// The lane's vectors into row p.
+template <typename T, int E, int V>
+__device__ __forceinline__ void store_row(T* p, const f2 (&v)[V * E / 2], const Team& t, int vecs) {
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const int c = t.first + k * t.step;
+    if (c >= vecs) continue;
+    T* q = p + c * E;
+    const int j = k * E / 2;
+    float lo, hi;
+    f2_unpack(v[j], lo, hi);
+    if constexpr (sizeof(T) == 2 && E == 8) {
+      *reinterpret_cast<uint4*>(q) = make_uint4(to_bf16_pair(v[j]), to_bf16_pair(v[j + 1]),
+                                                to_bf16_pair(v[j + 2]), to_bf16_pair(v[j + 3]));
+    } else if constexpr (sizeof(T) == 2 && E == 2) {
+      *reinterpret_cast<uint32_t*>(q) = to_bf16_pair(v[j]);
+    } else if constexpr (sizeof(T) == 4 && E == 4) {
+      float l1, h1;
+      f2_unpack(v[j + 1], l1, h1);
+      *reinterpret_cast<float4*>(q) = make_float4(lo, hi, l1, h1);
+    } else {
+      *q = from_f32<T>(k % 2 ? hi : lo);
+    }
+  }
+}
+
 // Sum over the lanes of a team inside a warp (over the warp for wider teams).
 template <bool WIDE>
 __device__ __forceinline__ float lanes_sum(float v, int lanes) {
@@ -359,44 +482,38 @@ __device__ __forceinline__ void team_barrier(const Team& t) {
   asm volatile("bar.sync %0, %1;" ::"r"(t.id + 1), "r"(t.lanes) : "memory");
 }
 
-template <typename T, int E, int V>
-__device__ __forceinline__ void load_row(Raw<T, E> (&raw)[V], const T* p, const Team& t, int vecs) {
-#pragma unroll
-  for (int k = 0; k < V; ++k) {
-    const int v = t.first + k * t.step;
-    if (v < vecs)
-      raw[k].load(p + v * E);
-    else
-      raw[k].zero();
-  }
-}
-template <typename T, int E, int V>
-__device__ __forceinline__ void zero_row(Raw<T, E> (&raw)[V]) {
-#pragma unroll
-  for (int k = 0; k < V; ++k) raw[k].zero();
+// The vector of a lane's element i lies in the row.
+template <int E>
+__device__ __forceinline__ bool in_row(const Team& t, int i, int vecs) {
+  return t.first + i / E * t.step < vecs;
 }
 
 // A lane's columns of a weight or bias vector; `none` without one, 0 behind the row.
 template <int E, int V>
-__device__ __forceinline__ void load_affine(float (&w)[V * E], const void* p, bool bf16, float none,
-                                            const Team& t, int vecs) {
+__device__ __forceinline__ void load_affine(f2 (&w)[V * E / 2], const void* p, bool bf16,
+                                            float none, const Team& t, int vecs) {
+  float v[V * E];
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    const int v = t.first + k * t.step;
+    const int64_t c = static_cast<int64_t>(t.first + k * t.step) * E;
 #pragma unroll
     for (int i = 0; i < E; ++i)
-      w[k * E + i] = v < vecs ? (p ? affine_at(p, bf16, static_cast<int64_t>(v) * E + i) : none)
-                              : 0.0f;
+      v[k * E + i] = in_row<E>(t, k * E, vecs) ? (p ? affine_at(p, bf16, c + i) : none) : 0.0f;
   }
+#pragma unroll
+  for (int i = 0; i < V * E; i += 2) w[i / 2] = f2_pack(v[i], v[i + 1]);
 }
 
 template <typename T, int E, int V, int ACT, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? kMaxRowWarps * 32 : kThreads, WIDE ? 1 : 3)
+__global__ void __launch_bounds__(WIDE ? kMaxRowWarps * 32 : kThreads,
+                                  WIDE ? 1 : kRowThreads / kThreads)
     norm_row_kernel(LayerNormArgs a, int lanes) {
   // warps' sums and squares, two buffers in turn: one is written again only behind the
   // other's barrier
-  __shared__ float2 slot[2][kMaxRowWarps];
+  __shared__ float2 slot[2][WIDE ? kMaxRowWarps : 1];
+  extern __shared__ __align__(16) uint8_t ring[];
   constexpr int N = V * E;
+  constexpr int S = kRowStages;
   pdl_wait();
   const Team t = team_of<V, WIDE>(lanes);
   const int vecs = a.c / E;
@@ -406,40 +523,49 @@ __global__ void __launch_bounds__(WIDE ? kMaxRowWarps * 32 : kThreads, WIDE ? 1 
   const float last_count = static_cast<float>(a.c - (t.warps - 1) * 32 * N);
   const float my_count = t.warp + 1 < t.warps ? 32.0f * N : last_count;
   const float inv_mine = 1.0f / my_count, inv_last = 1.0f / last_count;
-  float w[N], b[N];
-  load_affine<E, V>(w, a.weight, a.affine_bf16, 1.0f, t, vecs);
-  load_affine<E, V>(b, a.bias, a.affine_bf16, 0.0f, t, vecs);
   const T* x = static_cast<const T*>(a.x);
   T* y = static_cast<T*>(a.y);
-  Raw<T, E> next[V];
-  zero_row(next);
-  if (t.base + t.sub < a.n) load_row<T, E, V>(next, x + (t.base + t.sub) * a.x_stride, t, vecs);
-  int turn = 0;
+  Ahead<T, E, V> ahead;
+  ahead.init(smem_u32(ring));
+  const auto fetch = [&](int s, int64_t r) {
+    const bool live = r < a.n;
+    ahead.fetch(s, live ? x + r * a.x_stride : x, live, t, vecs);
+    if constexpr (ahead.kAsync) copies_commit();
+  };
+  constexpr int kFront = ahead.kAsync ? S - 1 : 1;  // rows on their way
+#pragma unroll
+  for (int s = 0; s < kFront; ++s) fetch(s, t.base + t.sub + s * t.stride);
+  f2 w[N / 2], b[N / 2];
+  load_affine<E, V>(w, a.weight, a.affine_bf16, 1.0f, t, vecs);
+  load_affine<E, V>(b, a.bias, a.affine_bf16, 0.0f, t, vecs);
+  int turn = 0, cur = 0;
   for (int64_t base = t.base; base < a.n; base += t.stride) {
     const int64_t r = base + t.sub;
-    float v[N];
+    f2 v[N / 2];
+    if constexpr (ahead.kAsync) copies_wait<S - 2>();
+    ahead.read(cur, v);
+    fetch(cur == 0 ? S - 1 : cur - 1, r + kFront * t.stride);
+    cur = cur + 1 == S ? 0 : cur + 1;
+    f2 s = v[0];
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = next[i / E].at(i % E);
-    if (r + t.stride < a.n) load_row<T, E, V>(next, x + (r + t.stride) * a.x_stride, t, vecs);
-    f2 s = f2_set(0.0f);
-#pragma unroll
-    for (int i = 0; i < N; i += 2) s = f2_add(s, f2_pack(v[i], v[i + 1]));
+    for (int i = 1; i < N / 2; ++i) s = f2_add(s, v[i]);
     const float sum = lanes_sum<WIDE>(f2_sum(s), lanes);
     float mean = sum * inv_mine;  // the warp's, and the row's in a team of one warp
     f2 q = f2_set(0.0f);
     const f2 shift = f2_set(-mean);
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      f2 d = f2_add(f2_pack(v[i], v[i + 1]), shift);
-      f2_unpack(d, v[i], v[i + 1]);
+    for (int i = 0; i < N / 2; ++i) {
+      v[i] = f2_add(v[i], shift);
       if (!full) {  // columns behind the row's end do not count
-        if (t.first + i / E * t.step >= vecs) v[i] = 0.0f;
-        if (t.first + (i + 1) / E * t.step >= vecs) v[i + 1] = 0.0f;
-        d = f2_pack(v[i], v[i + 1]);
+        float lo, hi;
+        f2_unpack(v[i], lo, hi);
+        v[i] = f2_pack(in_row<E>(t, 2 * i, vecs) ? lo : 0.0f,
+                       in_row<E>(t, 2 * i + 1, vecs) ? hi : 0.0f);
       }
-      q = f2_fma(d, d, q);
+      q = f2_fma(v[i], v[i], q);
     }
     float sq = lanes_sum<WIDE>(f2_sum(q), lanes);
+    f2 moved = f2_set(0.0f);
     if (WIDE) {
       // the squares around the row's mean from those around the warps' means
       const int first = t.id * t.warps;
@@ -456,32 +582,18 @@ __global__ void __launch_bounds__(WIDE ? kMaxRowWarps * 32 : kThreads, WIDE ? 1 
         sq += __fmaf_rn(d * d, end ? last_count : 32.0f * N, e.y);
       }
       turn ^= 1;
-      const f2 moved = f2_set(mean - whole);
-#pragma unroll
-      for (int i = 0; i < N; i += 2)
-        f2_unpack(f2_add(f2_pack(v[i], v[i + 1]), moved), v[i], v[i + 1]);
+      moved = f2_set(mean - whole);
       mean = whole;
     }
     const float rstd = 1.0f / sqrtf(__fmaf_rn(sq, inv_c, a.eps));
     const f2 rs = f2_set(rstd);
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      f2_unpack(f2_fma(f2_mul(f2_pack(v[i], v[i + 1]), rs), f2_pack(w[i], w[i + 1]),
-                       f2_pack(b[i], b[i + 1])),
-                v[i], v[i + 1]);
-      if (ACT == kActGelu) {
-        gelu_erf2(v[i], v[i + 1]);
-      } else {
-        v[i] = activate<ACT>(v[i]);
-        v[i + 1] = activate<ACT>(v[i + 1]);
-      }
+    for (int i = 0; i < N / 2; ++i) {
+      const f2 d = WIDE ? f2_add(v[i], moved) : v[i];
+      v[i] = act_pair<ACT>(f2_fma(f2_mul(d, rs), w[i], b[i]));
     }
     if (r < a.n) {
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const int c = t.first + k * t.step;
-        if (c < vecs) Raw<T, E>::store(y + r * a.c + c * E, &v[k * E]);
-      }
+      store_row<T, E, V>(y + r * a.c, v, t, vecs);
       if (a.mean && t.leader) {
         a.mean[r] = mean;
         a.rstd[r] = rstd;
@@ -493,67 +605,70 @@ __global__ void __launch_bounds__(WIDE ? kMaxRowWarps * 32 : kThreads, WIDE ? 1 
 // dx of the team's rows, and the block's column sums of dz xhat and dz into
 // partial[block][2][C] (or straight into dweight and dbias, for a grid of one).
 template <typename T, int E, int V, int ACT, bool WIDE>
-__global__ void __launch_bounds__(kMaxGradWarps * 32, 2)
+__global__ void __launch_bounds__(kMaxGradWarps * 32, kGradThreads / (kMaxGradWarps * 32))
     norm_grad_row_kernel(LayerNormGradArgs a, int lanes) {
-  __shared__ float2 slot[2][kMaxGradWarps];
-  extern __shared__ float sums[];  // [2][C]
+  __shared__ float2 slot[2][WIDE ? kMaxGradWarps : 1];
+  extern __shared__ __align__(16) uint8_t ring[];  // rows ahead; at the end the sums
   constexpr int N = V * E;
+  constexpr int S = kGradStages;
   pdl_wait();
   const Team t = team_of<V, WIDE>(lanes);
   const int vecs = a.c / E;
   const float inv_c = 1.0f / static_cast<float>(a.c);
-  float w[N], b[N], dw[N], db[N];
-  load_affine<E, V>(w, a.weight, a.affine_bf16, 1.0f, t, vecs);
-  if (ACT != kActNone) load_affine<E, V>(b, a.bias, a.affine_bf16, 0.0f, t, vecs);
-#pragma unroll
-  for (int i = 0; i < N; ++i) dw[i] = db[i] = 0.0f;
   const T* x = static_cast<const T*>(a.x);
   const T* dy = static_cast<const T*>(a.dy);
   T* dx = static_cast<T*>(a.dx);
-  Raw<T, E> nx[V], ny[V];
-  zero_row(nx);
-  zero_row(ny);
-  float next_mean = 0.0f, next_rstd = 0.0f;
-  const auto fetch = [&](int64_t r) {
-    next_mean = a.mean[r];
-    next_rstd = a.rstd[r];
-    load_row<T, E, V>(nx, x + r * a.x_stride, t, vecs);
-    load_row<T, E, V>(ny, dy + r * a.dy_stride, t, vecs);
+  Ahead<T, E, V> ax, ay;
+  constexpr int kRing = ax.kAsync ? S * V * ax.kBytes : 0;  // bytes a thread
+  ax.init(smem_u32(ring));
+  ay.init(smem_u32(ring) + blockDim.x * kRing);
+  const uint32_t stats = smem_u32(ring) + blockDim.x * 2 * kRing + threadIdx.x * 4;
+  const auto fetch = [&](int s, int64_t r) {
+    const bool live = r < a.n;
+    ax.fetch(s, live ? x + r * a.x_stride : x, live, t, vecs);
+    ay.fetch(s, live ? dy + r * a.dy_stride : dy, live, t, vecs);
+    const uint32_t at = stats + s * blockDim.x * 8;
+    const int bytes = live ? 4 : 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(at),
+                 "l"(a.mean + (live ? r : 0)), "r"(bytes)
+                 : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(at + blockDim.x * 4),
+                 "l"(a.rstd + (live ? r : 0)), "r"(bytes)
+                 : "memory");
+    copies_commit();
   };
-  if (t.base + t.sub < a.n) fetch(t.base + t.sub);
-  int turn = 0;
+  constexpr int kFront = ax.kAsync ? S - 1 : 1;  // rows on their way
+#pragma unroll
+  for (int s = 0; s < kFront; ++s) fetch(s, t.base + t.sub + s * t.stride);
+  f2 w[N / 2], b[N / 2], dw[N / 2], db[N / 2];
+  load_affine<E, V>(w, a.weight, a.affine_bf16, 1.0f, t, vecs);
+  if (ACT != kActNone) load_affine<E, V>(b, a.bias, a.affine_bf16, 0.0f, t, vecs);
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) dw[i] = db[i] = f2_set(0.0f);
+  int turn = 0, cur = 0;
   for (int64_t base = t.base; base < a.n; base += t.stride) {
     const int64_t r = base + t.sub;
-    const float rstd = next_rstd;
-    const f2 shift = f2_set(-next_mean), rs = f2_set(rstd);
-    f2 xh[N / 2], g[N / 2];
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      xh[i / 2] = f2_pack(nx[i / E].at(i % E), nx[(i + 1) / E].at((i + 1) % E));
-      g[i / 2] = f2_pack(ny[i / E].at(i % E), ny[(i + 1) / E].at((i + 1) % E));
-    }
-    if (r + t.stride < a.n) {
-      fetch(r + t.stride);
-    } else {  // a warp's last round may have teams without a row
-      zero_row(ny);
-    }
+    f2 h[N / 2], g[N / 2];
+    copies_wait<kFront - 1>();
+    ax.read(cur, h);
+    ay.read(cur, g);
+    float mean, rstd;
+    const uint32_t at = stats + cur * blockDim.x * 8;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(mean) : "r"(at) : "memory");
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(rstd) : "r"(at + blockDim.x * 4) : "memory");
+    fetch((cur + kFront) % S, r + kFront * t.stride);
+    cur = cur + 1 == S ? 0 : cur + 1;
+    const f2 shift = f2_set(-mean), rs = f2_set(rstd);
     f2 s0 = f2_set(0.0f), s1 = f2_set(0.0f);
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      const f2 h = f2_mul(f2_add(xh[i / 2], shift), rs);
-      const f2 wp = f2_pack(w[i], w[i + 1]);
-      f2 dz = g[i / 2];
-      if (ACT != kActNone) {
-        float z0, z1;
-        f2_unpack(f2_fma(h, wp, f2_pack(b[i], b[i + 1])), z0, z1);
-        dz = f2_mul(dz, f2_pack(act_slope_rt(ACT, z0), act_slope_rt(ACT, z1)));
-      }
-      f2_unpack(f2_add(f2_pack(db[i], db[i + 1]), dz), db[i], db[i + 1]);
-      f2_unpack(f2_fma(dz, h, f2_pack(dw[i], dw[i + 1])), dw[i], dw[i + 1]);
-      xh[i / 2] = h;
-      g[i / 2] = f2_mul(dz, wp);
-      s0 = f2_add(s0, g[i / 2]);
-      s1 = f2_fma(g[i / 2], h, s1);
+    for (int i = 0; i < N / 2; ++i) {
+      h[i] = f2_mul(f2_add(h[i], shift), rs);
+      if (ACT != kActNone) g[i] = f2_mul(g[i], slope_pair<ACT>(f2_fma(h[i], w[i], b[i])));
+      db[i] = f2_add(db[i], g[i]);
+      dw[i] = f2_fma(g[i], h[i], dw[i]);
+      g[i] = f2_mul(g[i], w[i]);
+      s0 = f2_add(s0, g[i]);
+      s1 = f2_fma(g[i], h[i], s1);
     }
     float m0 = lanes_sum<WIDE>(f2_sum(s0), lanes), m1 = lanes_sum<WIDE>(f2_sum(s1), lanes);
     if (WIDE) {
@@ -570,85 +685,77 @@ __global__ void __launch_bounds__(kMaxGradWarps * 32, 2)
     if (r < a.n && dx) {
       const f2 c0 = f2_set(-m0 * inv_c * rstd), c1 = f2_set(-m1 * inv_c * rstd);
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        float o[E];
-#pragma unroll
-        for (int i = 0; i < E; i += 2) {
-          if (E > 1) {
-            const int j = (k * E + i) / 2;
-            f2_unpack(f2_fma(xh[j], c1, f2_fma(g[j], rs, c0)), o[i], o[(i + 1) % E]);
-          } else {
-            float p0, p1;
-            f2_unpack(f2_fma(xh[k / 2], c1, f2_fma(g[k / 2], rs, c0)), p0, p1);
-            o[0] = k % 2 ? p1 : p0;
-          }
-        }
-        const int c = t.first + k * t.step;
-        if (c < vecs) Raw<T, E>::store(dx + r * a.c + c * E, o);
-      }
+      for (int i = 0; i < N / 2; ++i) g[i] = f2_fma(h[i], c1, f2_fma(g[i], rs, c0));
+      store_row<T, E, V>(dx + r * a.c, g, t, vecs);
     }
   }
   if (!a.partial) return;
-  // The lanes with the same columns: first the teams of a warp, then, one after
-  // another, the block's warps or wider teams.
+  // The lanes with the same columns: first the teams of a warp by shuffles, then the
+  // block's warps (or wider teams) through shared memory, where the rows' slots hold
+  // their sums now, [groups][2][C].
+  if (!WIDE) {
 #pragma unroll
-  for (int o = 16; o > 0; o /= 2)
-    if (!WIDE && o >= lanes) {
+    for (int o = 16; o > 0; o /= 2)
+      if (o >= lanes) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        dw[i] += __shfl_xor_sync(0xFFFFFFFFu, dw[i], o);
-        db[i] += __shfl_xor_sync(0xFFFFFFFFu, db[i], o);
-      }
-    }
-  const int rounds = WIDE ? blockDim.x / lanes : blockDim.x / 32;
-  const int mine = WIDE ? t.id : static_cast<int>(threadIdx.x) / 32;
-  for (int round = 0; round < rounds; ++round) {
-    if (round == mine && t.sub == 0) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int v = t.first + i / E * t.step;
-        if (v < vecs) {
-          float* p = sums + v * E + i % E;
-          p[0] = round ? p[0] + dw[i] : dw[i];
-          p[a.c] = round ? p[a.c] + db[i] : db[i];
+        for (int i = 0; i < N / 2; ++i) {
+          dw[i] = f2_add(dw[i], __shfl_xor_sync(0xFFFFFFFFu, dw[i], o));
+          db[i] = f2_add(db[i], __shfl_xor_sync(0xFFFFFFFFu, db[i], o));
         }
       }
-    }
-    __syncthreads();
   }
-  if (gridDim.x == 1) {
-    for (int c = threadIdx.x; c < a.c; c += blockDim.x) {
-      if (a.dweight) a.dweight[c] = sums[c];
-      if (a.dbias) a.dbias[c] = sums[a.c + c];
+  copies_wait<0>();
+  __syncthreads();
+  float* sums = reinterpret_cast<float*>(ring);
+  const int groups = WIDE ? blockDim.x / lanes : blockDim.x / 32;
+  if (t.sub == 0) {
+    float* mine = sums + (WIDE ? t.id : static_cast<int>(threadIdx.x) / 32) * 2 * a.c;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (!in_row<E>(t, i, vecs)) continue;
+      float lo, hi;
+      const int c = (t.first + i / E * t.step) * E + i % E;
+      f2_unpack(dw[i / 2], lo, hi);
+      mine[c] = i % 2 ? hi : lo;
+      f2_unpack(db[i / 2], lo, hi);
+      mine[a.c + c] = i % 2 ? hi : lo;
     }
-  } else {
-    float* p = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.c;
-    for (int c = threadIdx.x; c < 2 * a.c; c += blockDim.x) p[c] = sums[c];
+  }
+  __syncthreads();
+  float* partial = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.c;
+  for (int c = threadIdx.x; c < 2 * a.c; c += blockDim.x) {
+    float sum = sums[c];
+    for (int k = 1; k < groups; ++k) sum += sums[k * 2 * a.c + c];
+    if (gridDim.x > 1) {
+      partial[c] = sum;
+    } else {
+      float* out = c < a.c ? a.dweight : a.dbias;
+      if (out) out[c < a.c ? c : c - a.c] = sum;
+    }
   }
 }
 
 // How a row kernel lies on the rows.
 struct RowPlan {
-  int vec = 0;    // elements a load: 16 bytes' or 1
+  int vec = 0;    // elements a load
   int v = 0;      // loads a lane
   int lanes = 0;  // threads of a team; 0: the row is too wide
   int threads = 0;
   int64_t teams = 0;  // of a block
 };
 
-// Rows whose starts and width are multiples of 16 bytes take 16-byte loads.  A lane
-// holds 16 elements (8 or 4 single ones: a narrow row still spreads over lanes, and
-// a lane's columns cost registers); teams are as small as that allows.
-RowPlan row_plan(int32_t c, bool bf16, bool vector, int max_warps) {
+// Loads of 16 bytes where the rows' starts and widths are multiples of that, else of
+// 4 where they are (bf16), else of an element.  A lane holds 16 elements (8 single
+// ones); teams are as small as that allows.
+RowPlan row_plan(int32_t c, bool bf16, int align, int max_warps) {
   RowPlan p;
-  const int wide = bf16 ? 8 : 4;
-  p.vec = vector && c % wide == 0 ? wide : 1;
+  p.vec = align == 16 ? (bf16 ? 8 : 4) : (align == 4 && bf16 ? 2 : 1);
+  p.v = p.vec > 1 ? 16 / p.vec : 8;
   const int vecs = c / p.vec;
-  p.v = p.vec > 1 ? 16 / p.vec : (vecs <= 128 ? 4 : 8);
   if (vecs <= 32 * p.v) {
     p.lanes = 1;
     while (p.lanes * p.v < vecs) p.lanes *= 2;
-    p.threads = 256;
+    p.threads = kThreads;
   } else {
     const int warps = (vecs + 32 * p.v - 1) / (32 * p.v);
     if (warps > max_warps) return p;
@@ -662,77 +769,88 @@ RowPlan row_plan(int32_t c, bool bf16, bool vector, int max_warps) {
 
 // Blocks for n rows: as many as there are teams for, up to what fits on the device
 // at once (teams walk on from there) and `most`.
-template <typename Kernel>
-int64_t resident_blocks(Kernel kernel, const RowPlan& p, int64_t n, size_t smem, int num_sms,
-                        int64_t most) {
-  int per_sm = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, p.threads, smem) !=
-          cudaSuccess ||
-      per_sm < 1)
-    per_sm = 1;
-  return std::min({(n + p.teams - 1) / p.teams, static_cast<int64_t>(per_sm) * num_sms, most});
+int64_t blocks_for(const RowPlan& p, int64_t n, int sm_threads, int num_sms, int64_t most) {
+  const int64_t resident = static_cast<int64_t>(std::max(1, sm_threads / p.threads)) * num_sms;
+  return std::min({(n + p.teams - 1) / p.teams, resident, most});
 }
 
-bool rows_of_16_bytes(const void* p, int64_t stride, bool bf16) {
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % (bf16 ? 8 : 4) == 0;
+// The largest of 16, 4 and the element's bytes that every row's start is a multiple of.
+int rows_align(const void* p, int64_t stride, bool bf16) {
+  const uint64_t bytes = static_cast<uint64_t>(stride) * (bf16 ? 2 : 4);
+  const uint64_t both = reinterpret_cast<uintptr_t>(p) | bytes;
+  return both % 16 == 0 ? 16 : (both % 4 == 0 ? 4 : 2);
 }
 
-template <typename T, int E, int V>
+// More than 48 KB of shared memory, static included, is allowed to a kernel once a device.
+template <auto KERNEL>
+cudaError_t allow_smem(size_t bytes) {
+  if (bytes <= 47 * 1024) return cudaSuccess;
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
+template <typename T, int E, int V, int ACT, bool WIDE>
 cudaError_t launch_norm_rows(const LayerNormArgs& a, const RowPlan& p, int num_sms,
                              cudaStream_t stream) {
-  const auto go = [&](auto kernel) {
-    const int64_t blocks = resident_blocks(kernel, p, a.n, 0, num_sms, 0x7FFFFFFF);
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(p.threads), 0, stream, a,
-                      p.lanes);
-  };
-  const auto pick = [&](auto wide) {
-    constexpr bool W = decltype(wide)::value;
-    if (a.act == kActGelu) return go(norm_row_kernel<T, E, V, kActGelu, W>);
-    if (a.act == kActSilu) return go(norm_row_kernel<T, E, V, kActSilu, W>);
-    return go(norm_row_kernel<T, E, V, kActNone, W>);
-  };
-  return p.lanes > 32 ? pick(std::true_type{}) : pick(std::false_type{});
+  using A = Ahead<T, E, V>;
+  const size_t smem = A::kAsync ? static_cast<size_t>(p.threads) * kRowStages * V * A::kBytes : 0;
+  constexpr auto kernel = norm_row_kernel<T, E, V, ACT, WIDE>;
+  const cudaError_t e = allow_smem<kernel>(smem);
+  if (e != cudaSuccess) return e;
+  const int64_t blocks =
+      blocks_for(p, a.n, WIDE ? kWideRowThreads : kRowThreads, num_sms, 0x7FFFFFFF);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(p.threads), smem, stream, a,
+                    p.lanes);
 }
 
 // The gradient's row kernel and the join of its blocks' column sums.
-template <typename T, int E, int V>
+template <typename T, int E, int V, int ACT, bool WIDE>
 cudaError_t launch_grad_rows(const LayerNormGradArgs& a, const RowPlan& p, int num_sms,
                              cudaStream_t stream) {
-  const auto go = [&](auto kernel) {
-    const size_t smem = a.partial ? static_cast<size_t>(a.c) * 8 : 0;
-    const int64_t blocks = resident_blocks(kernel, p, a.n, smem, num_sms, layer_norm_chunks(a.n));
-    const cudaError_t e = launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)),
-                                     dim3(p.threads), smem, stream, a, p.lanes);
-    if (e != cudaSuccess || !a.partial || blocks == 1) return e;
-    return launch_pdl(norm_dw_join_kernel, dim3(static_cast<unsigned>((a.c + 31) / 32), 2),
-                      dim3(kThreads), 0, stream, static_cast<const float*>(a.partial),
-                      static_cast<int>(blocks), a.c, a.dweight, a.dbias);
-  };
-  const auto pick = [&](auto wide) {
-    constexpr bool W = decltype(wide)::value;
-    if (a.act == kActGelu) return go(norm_grad_row_kernel<T, E, V, kActGelu, W>);
-    if (a.act == kActSilu) return go(norm_grad_row_kernel<T, E, V, kActSilu, W>);
-    return go(norm_grad_row_kernel<T, E, V, kActNone, W>);
-  };
-  return p.lanes > 32 ? pick(std::true_type{}) : pick(std::false_type{});
+  using A = Ahead<T, E, V>;
+  const size_t rows = A::kAsync ? 2 * kGradStages * V * A::kBytes : 0;
+  const size_t groups = WIDE ? p.teams : p.threads / 32;
+  const size_t smem = std::max(static_cast<size_t>(p.threads) * (rows + kGradStages * 8),
+                               groups * a.c * 8);
+  constexpr auto kernel = norm_grad_row_kernel<T, E, V, ACT, WIDE>;
+  cudaError_t e = allow_smem<kernel>(smem);
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = blocks_for(p, a.n, kGradThreads, num_sms, layer_norm_chunks(a.n));
+  e = launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(p.threads), smem, stream, a,
+                 p.lanes);
+  if (e != cudaSuccess || !a.partial || blocks == 1) return e;
+  return launch_pdl(norm_dw_join_kernel, dim3(static_cast<unsigned>((a.c + 31) / 32), 2),
+                    dim3(kThreads), 0, stream, static_cast<const float*>(a.partial),
+                    static_cast<int>(blocks), a.c, a.dweight, a.dbias);
 }
 
-// f<T, E, V> of a plan.
-#define SUBM3D_ROW_PLAN(f, p, bf16, ...)                                        \
-  ((bf16) ? ((p).vec > 1 ? f<__nv_bfloat16, 8, 2>(__VA_ARGS__)                  \
-                         : ((p).v == 4 ? f<__nv_bfloat16, 1, 4>(__VA_ARGS__)    \
-                                       : f<__nv_bfloat16, 1, 8>(__VA_ARGS__))) \
-          : ((p).vec > 1 ? f<float, 4, 4>(__VA_ARGS__)                          \
-                         : ((p).v == 4 ? f<float, 1, 4>(__VA_ARGS__)            \
-                                       : f<float, 1, 8>(__VA_ARGS__))))
+// f<T, E, V, ACT, WIDE> of a plan.
+#define SUBM3D_ROW_WIDE(f, T, E, V, ACT, p, ...) \
+  ((p).lanes > 32 ? f<T, E, V, ACT, true>(__VA_ARGS__) : f<T, E, V, ACT, false>(__VA_ARGS__))
+#define SUBM3D_ROW_ACT(f, T, E, V, act, p, ...)                                        \
+  ((act) == kActGelu ? SUBM3D_ROW_WIDE(f, T, E, V, kActGelu, p, __VA_ARGS__)           \
+                     : ((act) == kActSilu ? SUBM3D_ROW_WIDE(f, T, E, V, kActSilu, p, __VA_ARGS__) \
+                                          : SUBM3D_ROW_WIDE(f, T, E, V, kActNone, p, __VA_ARGS__)))
+#define SUBM3D_ROW_PLAN(f, a, p, ...)                                                         \
+  ((a).bf16 ? ((p).vec == 8 ? SUBM3D_ROW_ACT(f, __nv_bfloat16, 8, 2, (a).act, p, __VA_ARGS__) \
+               : (p).vec == 2 ? SUBM3D_ROW_ACT(f, __nv_bfloat16, 2, 8, (a).act, p, __VA_ARGS__) \
+                              : SUBM3D_ROW_ACT(f, __nv_bfloat16, 1, 8, (a).act, p, __VA_ARGS__)) \
+            : ((p).vec == 4 ? SUBM3D_ROW_ACT(f, float, 4, 4, (a).act, p, __VA_ARGS__)         \
+                            : SUBM3D_ROW_ACT(f, float, 1, 8, (a).act, p, __VA_ARGS__)))
 
 }  // namespace
 
 cudaError_t launch_layer_norm(const LayerNormArgs& a, int num_sms, cudaStream_t stream) {
-  const bool vector =
-      rows_of_16_bytes(a.x, a.x_stride, a.bf16) && rows_of_16_bytes(a.y, a.c, a.bf16);
-  const RowPlan p = row_plan(a.c, a.bf16, vector, kMaxRowWarps);
-  if (p.lanes > 0) return SUBM3D_ROW_PLAN(launch_norm_rows, p, a.bf16, a, p, num_sms, stream);
+  const int align = std::min(rows_align(a.x, a.x_stride, a.bf16), rows_align(a.y, a.c, a.bf16));
+  const RowPlan p = row_plan(a.c, a.bf16, align, kMaxRowWarps);
+  if (p.lanes > 0) return SUBM3D_ROW_PLAN(launch_norm_rows, a, p, a, p, num_sms, stream);
   const dim3 grid(static_cast<unsigned>(std::min(a.n, static_cast<int64_t>(num_sms) * 8)));
   return a.bf16 ? launch_pdl(norm_any_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, stream, a)
                 : launch_pdl(norm_any_kernel<float>, grid, dim3(kThreads), 0, stream, a);
@@ -742,11 +860,11 @@ cudaError_t launch_layer_norm_grad(const LayerNormGradArgs& in, int num_sms, cud
   cudaError_t e = cudaSuccess;
   LayerNormGradArgs a = in;
   if (!a.dweight && !a.dbias) a.partial = nullptr;
-  const bool vector = rows_of_16_bytes(a.x, a.x_stride, a.bf16) &&
-                      rows_of_16_bytes(a.dy, a.dy_stride, a.bf16) &&
-                      rows_of_16_bytes(a.dx, a.c, a.bf16);
-  const RowPlan p = row_plan(a.c, a.bf16, vector, kMaxGradWarps);
-  if (p.lanes > 0) return SUBM3D_ROW_PLAN(launch_grad_rows, p, a.bf16, a, p, num_sms, stream);
+  const int align = std::min({rows_align(a.x, a.x_stride, a.bf16),
+                              rows_align(a.dy, a.dy_stride, a.bf16),
+                              rows_align(a.dx, a.c, a.bf16)});
+  const RowPlan p = row_plan(a.c, a.bf16, align, kMaxGradWarps);
+  if (p.lanes > 0) return SUBM3D_ROW_PLAN(launch_grad_rows, a, p, a, p, num_sms, stream);
   if (a.dx) {
     const int64_t blocks = std::min(a.n, static_cast<int64_t>(num_sms) * 8);
     const dim3 grid(static_cast<unsigned>(blocks));
