@@ -256,6 +256,7 @@ struct LayerNormArgs {
   int64_t n = 0, x_stride = 0;
   int32_t c = 0, act = 0;
   float eps = 0.0f;
+  uint32_t row_bytes = 0;  // x_stride in bytes (set by the launch)
   bool bf16 = false, affine_bf16 = false;
 };
 cudaError_t launch_layer_norm(const LayerNormArgs& a, int num_sms, cudaStream_t stream);
@@ -275,6 +276,7 @@ struct LayerNormGradArgs {
   float* partial = nullptr;
   int64_t n = 0, x_stride = 0, dy_stride = 0;
   int32_t c = 0, act = 0;
+  uint32_t x_row_bytes = 0, dy_row_bytes = 0;  // the strides in bytes (set by the launch)
   bool bf16 = false, affine_bf16 = false;
 };
 int64_t layer_norm_chunks(int64_t n);

@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kThreads) norm_dw_join_kernel(const float* par
 
 // ---------------------------------------------------------------- row kernels ----
 //
-// A team works on one row: 2^k lanes of a warp, or several whole warps (WIDE).  A
+// A team works on one row: 2^k lanes of a warp, or several whole warps (WIDE; LANES = 0).  A
 // lane holds N = V x E elements of the row: V loads of E elements, as wide as the
 // rows' alignment allows.  The row is read once; its sums go over the team by
 // shuffles, and between warps through one exchange in shared memory.  Teams walk
@@ -248,6 +248,9 @@ __global__ void __launch_bounds__(kThreads) norm_dw_join_kernel(const float* par
 constexpr int kRowStages = KS, kGradStages = KG;
 constexpr int kMaxRowWarps = 16;  // forward: rows up to 16 * 32 * 16 = 8,192 elements
 constexpr int kMaxGradWarps = 8;  // backward: 4,096
+// Rows are counted in 32 bits, some strides of all teams beyond the last one included.
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - (1 << 20);
+constexpr int kFewestLanes = 4;   // of a team: 16 bytes of 64 channels a lane and load
 // Resident threads on an SM that the kernels' register bounds allow.
 constexpr int kRowThreads = 768, kWideRowThreads = 512, kGradThreads = 512;
 
@@ -336,20 +339,21 @@ __device__ __forceinline__ f2 slope_pair(f2 z) {
 }
 
 // A thread's place.  `lanes` = threads of a team: a power of two up to 32, or whole
-// warps.  The loop over rows is a warp's: `base` is its first team's row, and rows
-// from a.n on (the last round of teams inside a warp) are computed on zeros and not
-// stored, so that all lanes take part in every shuffle.
+// warps.  The loop over rows is a warp's: rows from a.n on (the last round of teams
+// inside a warp) are computed on zeros and not stored, so that all lanes take part in
+// every shuffle.
 struct Team {
   int lanes, warps;      // warps: of a team of whole warps, else 1
   int first, step;       // the lane's vectors: first + k step
   int warp;              // the warp's number in its team
   int id;                // the team's number in the block
   bool leader;           // the team's first lane
-  int64_t base, stride;  // the loop over rows
+  uint32_t row, stride;  // the loop over rows (below 2^31)
   int sub;               // the team's number in the warp
 };
-template <int V, bool WIDE>
+template <int V, int LANES>
 __device__ __forceinline__ Team team_of(int lanes) {
+  constexpr bool WIDE = LANES == 0;
   Team t;
   const int l = threadIdx.x % lanes;
   t.lanes = lanes;
@@ -361,65 +365,96 @@ __device__ __forceinline__ Team team_of(int lanes) {
   t.warp = WIDE ? l / 32 : 0;
   t.first = t.warp * 32 * V + l % t.step;
   t.sub = WIDE ? 0 : (threadIdx.x % 32) / lanes;
-  t.base = static_cast<int64_t>(blockIdx.x) * teams + (t.id - t.sub);
-  t.stride = static_cast<int64_t>(gridDim.x) * teams;
+  t.row = blockIdx.x * teams + t.id;
+  t.stride = gridDim.x * teams;
   return t;
 }
 
 // A lane's parts of the rows ahead.  Parts of 4, 8 or 16 bytes are copied into the
-// lane's own shared-memory slots; single bf16 elements (odd widths) are held in
-// registers, one row ahead.
-template <typename T, int E, int V>
+// lane's own shared-memory slots (S stages, at byte offsets 0, kStage, ... of a
+// thread's slot); single bf16 elements (odd widths) are held in registers, one row
+// ahead.  THREADS: the block's, 0 where it is not a constant.
+template <typename T, int E, int V, int S, int THREADS>
 struct Ahead {
   static constexpr int kBytes = static_cast<int>(sizeof(T)) * E;
   static constexpr bool kAsync = kBytes >= 4;
   static constexpr int N = V * E;
-  uint32_t mine, stage;  // addresses: slot of stage 0, bytes between stages
+  static constexpr int kFront = kAsync ? S - 1 : 1;  // rows on their way
+  const char* src;  // the lane's first vector of row 0
+  uint32_t mine;
   uint32_t held[kAsync ? 1 : V];
+  bool on[V];        // the vector lies in the row
 
-  __device__ __forceinline__ void init(uint32_t smem) {
+  static __device__ __forceinline__ uint32_t threads() { return THREADS ? THREADS : blockDim.x; }
+  static __device__ __forceinline__ uint32_t stage_bytes() { return threads() * V * kBytes; }
+
+  __device__ __forceinline__ void init(uint32_t smem, const void* x, const Team& t, int vecs) {
     mine = smem + threadIdx.x * kBytes;
-    stage = blockDim.x * V * kBytes;
-  }
-  // Starts on row p (zeros where `live` is false and behind the row's end).
-  __device__ __forceinline__ void fetch(int s, const T* p, bool live, const Team& t, int vecs) {
+    src = static_cast<const char*>(x) + static_cast<int64_t>(t.first) * kBytes;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const int v = t.first + k * t.step;
-      const bool on = live && v < vecs;
-      if constexpr (kAsync) {
-        const uint32_t dst = mine + s * stage + k * blockDim.x * kBytes;
-        const T* src = on ? p + v * E : p;
-        const int bytes = on ? kBytes : 0;
-        if constexpr (kBytes == 16)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                       "r"(bytes)
-                       : "memory");
-        else
-          asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src),
-                       "n"(kBytes), "r"(bytes)
-                       : "memory");
-      } else {
-        uint16_t h = 0;
-        if (on) asm volatile("ld.global.b16 %0, [%1];" : "=h"(h) : "l"(p + v));
-        held[k] = h;
+      on[k] = t.first + k * t.step < vecs;
+      if (!on[k]) {  // columns behind the row's end are zeros for good
+        held[kAsync ? 0 : k] = 0u;
+        if constexpr (kAsync)
+          for (int s = 0; s < S; ++s) zero(s * stage_bytes(), k);
       }
     }
   }
-  __device__ __forceinline__ void read(int s, f2 (&v)[N / 2]) const {
+  __device__ __forceinline__ void zero(uint32_t at, int k) {
+    const uint32_t dst = mine + at + k * threads() * kBytes;
+#pragma unroll
+    for (int i = 0; i < kBytes; i += 4)
+      asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + i), "r"(0) : "memory");
+  }
+  // Starts on row r, into the stage at byte offset `at`; zeros where there is none.
+  __device__ __forceinline__ void fetch(uint32_t at, uint32_t r, uint32_t row_bytes, bool live,
+                                        const Team& t) {
+    if (live) {
+      const char* row = src + static_cast<uint64_t>(r) * row_bytes;
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const char* p = row + k * t.step * kBytes;
+        if (!on[k]) continue;
+        if constexpr (!kAsync) {
+          uint16_t h;
+          asm volatile("ld.global.b16 %0, [%1];" : "=h"(h) : "l"(p));
+          held[k] = h;
+        } else {
+          const uint32_t dst = mine + at + k * threads() * kBytes;
+          if constexpr (kBytes == 16)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(p)
+                         : "memory");
+          else
+            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(p),
+                         "n"(kBytes)
+                         : "memory");
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        if constexpr (kAsync)
+          zero(at, k);
+        else
+          held[k] = 0u;
+      }
+    }
+  }
+  __device__ __forceinline__ void read(uint32_t at, f2 (&v)[N / 2]) const {
     uint32_t w[kAsync ? V * kBytes / 4 : V];
     if constexpr (kAsync) {
 #pragma unroll
       for (int k = 0; k < V; ++k) {
-        const uint32_t src = mine + s * stage + k * blockDim.x * kBytes;
+        const uint32_t from = mine + at + k * threads() * kBytes;
         uint32_t* o = w + k * kBytes / 4;
         if constexpr (kBytes == 16)
           asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
-                       : "r"(src)
+                       : "r"(from)
                        : "memory");
         else
-          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(o[0]) : "r"(src) : "memory");
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(o[0]) : "r"(from) : "memory");
       }
     } else {
 #pragma unroll
@@ -442,14 +477,14 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
 
-// The lane's vectors into row p.
+// The lane's vectors into its row, p = where its first one goes.
 template <typename T, int E, int V>
-__device__ __forceinline__ void store_row(T* p, const f2 (&v)[V * E / 2], const Team& t, int vecs) {
+__device__ __forceinline__ void store_row(T* p, const f2 (&v)[V * E / 2], const bool (&on)[V],
+                                          const Team& t) {
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    const int c = t.first + k * t.step;
-    if (c >= vecs) continue;
-    T* q = p + c * E;
+    if (!on[k]) continue;
+    T* q = p + k * t.step * E;
     const int j = k * E / 2;
     float lo, hi;
     f2_unpack(v[j], lo, hi);
@@ -469,23 +504,17 @@ __device__ __forceinline__ void store_row(T* p, const f2 (&v)[V * E / 2], const 
 }
 
 // Sum over the lanes of a team inside a warp (over the warp for wider teams).
-template <bool WIDE>
-__device__ __forceinline__ float lanes_sum(float v, int lanes) {
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
   for (int o = 1; o < 32; o *= 2)
-    if (WIDE || lanes > o) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if (LANES == 0 || LANES > o) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
 
 // The barrier of one team of several warps (barrier 0 is __syncthreads').
 __device__ __forceinline__ void team_barrier(const Team& t) {
   asm volatile("bar.sync %0, %1;" ::"r"(t.id + 1), "r"(t.lanes) : "memory");
-}
-
-// The vector of a lane's element i lies in the row.
-template <int E>
-__device__ __forceinline__ bool in_row(const Team& t, int i, int vecs) {
-  return t.first + i / E * t.step < vecs;
 }
 
 // A lane's columns of a weight or bias vector; `none` without one, 0 behind the row.
@@ -498,16 +527,18 @@ __device__ __forceinline__ void load_affine(f2 (&w)[V * E / 2], const void* p, b
     const int64_t c = static_cast<int64_t>(t.first + k * t.step) * E;
 #pragma unroll
     for (int i = 0; i < E; ++i)
-      v[k * E + i] = in_row<E>(t, k * E, vecs) ? (p ? affine_at(p, bf16, c + i) : none) : 0.0f;
+      v[k * E + i] = t.first + k * t.step < vecs ? (p ? affine_at(p, bf16, c + i) : none) : 0.0f;
   }
 #pragma unroll
   for (int i = 0; i < V * E; i += 2) w[i / 2] = f2_pack(v[i], v[i + 1]);
 }
 
-template <typename T, int E, int V, int ACT, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? kMaxRowWarps * 32 : kThreads,
-                                  WIDE ? 1 : kRowThreads / kThreads)
-    norm_row_kernel(LayerNormArgs a, int lanes) {
+template <typename T, int E, int V, int ACT, int LANES>
+__global__ void __launch_bounds__(LANES == 0 ? kMaxRowWarps * 32 : kThreads,
+                                  LANES == 0 ? 1 : kRowThreads / kThreads)
+    norm_row_kernel(LayerNormArgs a, int team_lanes) {
+  constexpr bool WIDE = LANES == 0;
+  const int lanes = WIDE ? team_lanes : LANES;
   // warps' sums and squares, two buffers in turn: one is written again only behind the
   // other's barrier
   __shared__ float2 slot[2][WIDE ? kMaxRowWarps : 1];
@@ -515,7 +546,7 @@ __global__ void __launch_bounds__(WIDE ? kMaxRowWarps * 32 : kThreads,
   constexpr int N = V * E;
   constexpr int S = kRowStages;
   pdl_wait();
-  const Team t = team_of<V, WIDE>(lanes);
+  const Team t = team_of<V, LANES>(lanes);
   const int vecs = a.c / E;
   const bool full = vecs == V * lanes;
   const float inv_c = 1.0f / static_cast<float>(a.c);
@@ -523,48 +554,50 @@ __global__ void __launch_bounds__(WIDE ? kMaxRowWarps * 32 : kThreads,
   const float last_count = static_cast<float>(a.c - (t.warps - 1) * 32 * N);
   const float my_count = t.warp + 1 < t.warps ? 32.0f * N : last_count;
   const float inv_mine = 1.0f / my_count, inv_last = 1.0f / last_count;
-  const T* x = static_cast<const T*>(a.x);
-  T* y = static_cast<T*>(a.y);
-  Ahead<T, E, V> ahead;
-  ahead.init(smem_u32(ring));
-  const auto fetch = [&](int s, int64_t r) {
-    const bool live = r < a.n;
-    ahead.fetch(s, live ? x + r * a.x_stride : x, live, t, vecs);
-    if constexpr (ahead.kAsync) copies_commit();
+  using A = Ahead<T, E, V, S, WIDE ? 0 : kThreads>;
+  A ahead;
+  ahead.init(smem_u32(ring), a.x, t, vecs);
+  const uint32_t n = static_cast<uint32_t>(a.n);
+  const auto fetch = [&](uint32_t at, uint32_t r) {
+    ahead.fetch(at, r, a.row_bytes, r < n, t);
+    if constexpr (A::kAsync) copies_commit();
   };
-  constexpr int kFront = ahead.kAsync ? S - 1 : 1;  // rows on their way
+  const uint32_t stage = A::stage_bytes(), last_stage = (S - 1) * stage;
 #pragma unroll
-  for (int s = 0; s < kFront; ++s) fetch(s, t.base + t.sub + s * t.stride);
+  for (int s = 0; s < A::kFront; ++s) fetch(s * stage, t.row + s * t.stride);
   f2 w[N / 2], b[N / 2];
   load_affine<E, V>(w, a.weight, a.affine_bf16, 1.0f, t, vecs);
   load_affine<E, V>(b, a.bias, a.affine_bf16, 0.0f, t, vecs);
-  int turn = 0, cur = 0;
-  for (int64_t base = t.base; base < a.n; base += t.stride) {
-    const int64_t r = base + t.sub;
+  T* y = static_cast<T*>(a.y) + t.first * E;
+  int turn = 0;
+  uint32_t cur = 0, freed = last_stage;
+  for (uint32_t r = t.row; r - t.sub < n; r += t.stride) {
     f2 v[N / 2];
-    if constexpr (ahead.kAsync) copies_wait<S - 2>();
+    if constexpr (A::kAsync) copies_wait<A::kFront - 1>();
     ahead.read(cur, v);
-    fetch(cur == 0 ? S - 1 : cur - 1, r + kFront * t.stride);
-    cur = cur + 1 == S ? 0 : cur + 1;
+    fetch(freed, r + A::kFront * t.stride);
+    freed = cur;
+    cur = cur == last_stage ? 0 : cur + stage;
     f2 s = v[0];
 #pragma unroll
     for (int i = 1; i < N / 2; ++i) s = f2_add(s, v[i]);
-    const float sum = lanes_sum<WIDE>(f2_sum(s), lanes);
+    const float sum = lanes_sum<LANES>(f2_sum(s));
     float mean = sum * inv_mine;  // the warp's, and the row's in a team of one warp
     f2 q = f2_set(0.0f);
     const f2 shift = f2_set(-mean);
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-      v[i] = f2_add(v[i], shift);
-      if (!full) {  // columns behind the row's end do not count
+    for (int i = 0; i < N / 2; ++i) v[i] = f2_add(v[i], shift);
+    if (!full) {  // columns behind the row's end do not count
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
         float lo, hi;
         f2_unpack(v[i], lo, hi);
-        v[i] = f2_pack(in_row<E>(t, 2 * i, vecs) ? lo : 0.0f,
-                       in_row<E>(t, 2 * i + 1, vecs) ? hi : 0.0f);
+        v[i] = f2_pack(ahead.on[2 * i / E] ? lo : 0.0f, ahead.on[(2 * i + 1) / E] ? hi : 0.0f);
       }
-      q = f2_fma(v[i], v[i], q);
     }
-    float sq = lanes_sum<WIDE>(f2_sum(q), lanes);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) q = f2_fma(v[i], v[i], q);
+    float sq = lanes_sum<LANES>(f2_sum(q));
     f2 moved = f2_set(0.0f);
     if (WIDE) {
       // the squares around the row's mean from those around the warps' means
@@ -585,15 +618,15 @@ __global__ void __launch_bounds__(WIDE ? kMaxRowWarps * 32 : kThreads,
       moved = f2_set(mean - whole);
       mean = whole;
     }
-    const float rstd = 1.0f / sqrtf(__fmaf_rn(sq, inv_c, a.eps));
+    const float rstd = rsqrtf(__fmaf_rn(sq, inv_c, a.eps));
     const f2 rs = f2_set(rstd);
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
       const f2 d = WIDE ? f2_add(v[i], moved) : v[i];
       v[i] = act_pair<ACT>(f2_fma(f2_mul(d, rs), w[i], b[i]));
     }
-    if (r < a.n) {
-      store_row<T, E, V>(y + r * a.c, v, t, vecs);
+    if (r < n) {
+      store_row<T, E, V>(y + static_cast<uint64_t>(r) * static_cast<uint32_t>(a.c), v, ahead.on, t);
       if (a.mean && t.leader) {
         a.mean[r] = mean;
         a.rstd[r] = rstd;
@@ -604,60 +637,75 @@ __global__ void __launch_bounds__(WIDE ? kMaxRowWarps * 32 : kThreads,
 
 // dx of the team's rows, and the block's column sums of dz xhat and dz into
 // partial[block][2][C] (or straight into dweight and dbias, for a grid of one).
-template <typename T, int E, int V, int ACT, bool WIDE>
+template <typename T, int E, int V, int ACT, int LANES>
 __global__ void __launch_bounds__(kMaxGradWarps * 32, kGradThreads / (kMaxGradWarps * 32))
-    norm_grad_row_kernel(LayerNormGradArgs a, int lanes) {
+    norm_grad_row_kernel(LayerNormGradArgs a, int team_lanes) {
+  constexpr bool WIDE = LANES == 0;
+  const int lanes = WIDE ? team_lanes : LANES;
   __shared__ float2 slot[2][WIDE ? kMaxGradWarps : 1];
   extern __shared__ __align__(16) uint8_t ring[];  // rows ahead; at the end the sums
   constexpr int N = V * E;
   constexpr int S = kGradStages;
   pdl_wait();
-  const Team t = team_of<V, WIDE>(lanes);
+  const Team t = team_of<V, LANES>(lanes);
   const int vecs = a.c / E;
   const float inv_c = 1.0f / static_cast<float>(a.c);
-  const T* x = static_cast<const T*>(a.x);
-  const T* dy = static_cast<const T*>(a.dy);
-  T* dx = static_cast<T*>(a.dx);
-  Ahead<T, E, V> ax, ay;
-  constexpr int kRing = ax.kAsync ? S * V * ax.kBytes : 0;  // bytes a thread
-  ax.init(smem_u32(ring));
-  ay.init(smem_u32(ring) + blockDim.x * kRing);
-  const uint32_t stats = smem_u32(ring) + blockDim.x * 2 * kRing + threadIdx.x * 4;
-  const auto fetch = [&](int s, int64_t r) {
-    const bool live = r < a.n;
-    ax.fetch(s, live ? x + r * a.x_stride : x, live, t, vecs);
-    ay.fetch(s, live ? dy + r * a.dy_stride : dy, live, t, vecs);
-    const uint32_t at = stats + s * blockDim.x * 8;
-    const int bytes = live ? 4 : 0;
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(at),
-                 "l"(a.mean + (live ? r : 0)), "r"(bytes)
-                 : "memory");
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(at + blockDim.x * 4),
-                 "l"(a.rstd + (live ? r : 0)), "r"(bytes)
-                 : "memory");
+  using A = Ahead<T, E, V, S, WIDE ? 0 : kThreads>;
+  A ax, ay;
+  constexpr int kRing = A::kAsync ? S * V * A::kBytes : 0;  // bytes a thread
+  const uint32_t threads = A::threads();
+  ax.init(smem_u32(ring), a.x, t, vecs);
+  ay.init(smem_u32(ring) + threads * kRing, a.dy, t, vecs);
+  // a row's mean and rstd, fetched with it
+  const uint32_t stats = smem_u32(ring) + threads * 2 * kRing + threadIdx.x * 4;
+  constexpr uint32_t kRowBytes = A::kAsync ? V * A::kBytes : 8;  // a stage, per thread
+  const uint32_t n = static_cast<uint32_t>(a.n);
+  // stages are told apart by the byte offset of their rows' slots (single elements,
+  // which are not copied: by that of their statistics)
+  const auto stats_at = [&](uint32_t at) { return stats + at / kRowBytes * 8; };
+  const auto fetch = [&](uint32_t at, uint32_t r) {
+    const bool live = r < n;
+    ax.fetch(at, r, a.x_row_bytes, live, t);
+    ay.fetch(at, r, a.dy_row_bytes, live, t);
+    const uint32_t to = stats_at(at);
+    if (live) {
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(a.mean + r)
+                   : "memory");
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + threads * 4),
+                   "l"(a.rstd + r)
+                   : "memory");
+    } else {
+      asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(0) : "memory");
+      asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + threads * 4), "r"(0) : "memory");
+    }
     copies_commit();
   };
-  constexpr int kFront = ax.kAsync ? S - 1 : 1;  // rows on their way
+  const uint32_t stage = threads * kRowBytes;
+  const uint32_t last_stage = A::kFront * stage;
 #pragma unroll
-  for (int s = 0; s < kFront; ++s) fetch(s, t.base + t.sub + s * t.stride);
+  for (int s = 0; s < A::kFront; ++s) fetch(s * stage, t.row + s * t.stride);
   f2 w[N / 2], b[N / 2], dw[N / 2], db[N / 2];
   load_affine<E, V>(w, a.weight, a.affine_bf16, 1.0f, t, vecs);
   if (ACT != kActNone) load_affine<E, V>(b, a.bias, a.affine_bf16, 0.0f, t, vecs);
 #pragma unroll
   for (int i = 0; i < N / 2; ++i) dw[i] = db[i] = f2_set(0.0f);
-  int turn = 0, cur = 0;
-  for (int64_t base = t.base; base < a.n; base += t.stride) {
-    const int64_t r = base + t.sub;
+  T* dx = static_cast<T*>(a.dx) + t.first * E;
+  int turn = 0;
+  uint32_t cur = 0, freed = last_stage;
+  for (uint32_t r = t.row; r - t.sub < n; r += t.stride) {
     f2 h[N / 2], g[N / 2];
-    copies_wait<kFront - 1>();
+    copies_wait<A::kFront - 1>();
     ax.read(cur, h);
     ay.read(cur, g);
     float mean, rstd;
-    const uint32_t at = stats + cur * blockDim.x * 8;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(mean) : "r"(at) : "memory");
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(rstd) : "r"(at + blockDim.x * 4) : "memory");
-    fetch((cur + kFront) % S, r + kFront * t.stride);
-    cur = cur + 1 == S ? 0 : cur + 1;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(mean) : "r"(stats_at(cur)) : "memory");
+    asm volatile("ld.shared.f32 %0, [%1];"
+                 : "=f"(rstd)
+                 : "r"(stats_at(cur) + threads * 4)
+                 : "memory");
+    fetch(freed, r + A::kFront * t.stride);
+    freed = cur;
+    cur = cur == last_stage ? 0 : cur + stage;
     const f2 shift = f2_set(-mean), rs = f2_set(rstd);
     f2 s0 = f2_set(0.0f), s1 = f2_set(0.0f);
 #pragma unroll
@@ -670,7 +718,7 @@ __global__ void __launch_bounds__(kMaxGradWarps * 32, kGradThreads / (kMaxGradWa
       s0 = f2_add(s0, g[i]);
       s1 = f2_fma(g[i], h[i], s1);
     }
-    float m0 = lanes_sum<WIDE>(f2_sum(s0), lanes), m1 = lanes_sum<WIDE>(f2_sum(s1), lanes);
+    float m0 = lanes_sum<LANES>(f2_sum(s0)), m1 = lanes_sum<LANES>(f2_sum(s1));
     if (WIDE) {
       const int first = t.id * t.warps;
       if (threadIdx.x % 32 == 0) slot[turn][first + t.warp] = make_float2(m0, m1);
@@ -682,11 +730,11 @@ __global__ void __launch_bounds__(kMaxGradWarps * 32, kGradThreads / (kMaxGradWa
       }
       turn ^= 1;
     }
-    if (r < a.n && dx) {
+    if (r < n && a.dx) {
       const f2 c0 = f2_set(-m0 * inv_c * rstd), c1 = f2_set(-m1 * inv_c * rstd);
 #pragma unroll
       for (int i = 0; i < N / 2; ++i) g[i] = f2_fma(h[i], c1, f2_fma(g[i], rs, c0));
-      store_row<T, E, V>(dx + r * a.c, g, t, vecs);
+      store_row<T, E, V>(dx + static_cast<uint64_t>(r) * static_cast<uint32_t>(a.c), g, ax.on, t);
     }
   }
   if (!a.partial) return;
@@ -712,7 +760,7 @@ __global__ void __launch_bounds__(kMaxGradWarps * 32, kGradThreads / (kMaxGradWa
     float* mine = sums + (WIDE ? t.id : static_cast<int>(threadIdx.x) / 32) * 2 * a.c;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if (!in_row<E>(t, i, vecs)) continue;
+      if (!ax.on[i / E]) continue;
       float lo, hi;
       const int c = (t.first + i / E * t.step) * E + i % E;
       f2_unpack(dw[i / 2], lo, hi);
@@ -753,7 +801,7 @@ RowPlan row_plan(int32_t c, bool bf16, int align, int max_warps) {
   p.v = p.vec > 1 ? 16 / p.vec : 8;
   const int vecs = c / p.vec;
   if (vecs <= 32 * p.v) {
-    p.lanes = 1;
+    p.lanes = kFewestLanes;
     while (p.lanes * p.v < vecs) p.lanes *= 2;
     p.threads = kThreads;
   } else {
@@ -796,30 +844,30 @@ cudaError_t allow_smem(size_t bytes) {
   return e;
 }
 
-template <typename T, int E, int V, int ACT, bool WIDE>
+template <typename T, int E, int V, int ACT, int LANES>
 cudaError_t launch_norm_rows(const LayerNormArgs& a, const RowPlan& p, int num_sms,
                              cudaStream_t stream) {
-  using A = Ahead<T, E, V>;
+  using A = Ahead<T, E, V, kRowStages, 0>;
   const size_t smem = A::kAsync ? static_cast<size_t>(p.threads) * kRowStages * V * A::kBytes : 0;
-  constexpr auto kernel = norm_row_kernel<T, E, V, ACT, WIDE>;
+  constexpr auto kernel = norm_row_kernel<T, E, V, ACT, LANES>;
   const cudaError_t e = allow_smem<kernel>(smem);
   if (e != cudaSuccess) return e;
   const int64_t blocks =
-      blocks_for(p, a.n, WIDE ? kWideRowThreads : kRowThreads, num_sms, 0x7FFFFFFF);
+      blocks_for(p, a.n, LANES == 0 ? kWideRowThreads : kRowThreads, num_sms, 0x7FFFFFFF);
   return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(p.threads), smem, stream, a,
                     p.lanes);
 }
 
 // The gradient's row kernel and the join of its blocks' column sums.
-template <typename T, int E, int V, int ACT, bool WIDE>
+template <typename T, int E, int V, int ACT, int LANES>
 cudaError_t launch_grad_rows(const LayerNormGradArgs& a, const RowPlan& p, int num_sms,
                              cudaStream_t stream) {
-  using A = Ahead<T, E, V>;
+  using A = Ahead<T, E, V, kGradStages, 0>;
   const size_t rows = A::kAsync ? 2 * kGradStages * V * A::kBytes : 0;
-  const size_t groups = WIDE ? p.teams : p.threads / 32;
+  const size_t groups = LANES == 0 ? p.teams : p.threads / 32;
   const size_t smem = std::max(static_cast<size_t>(p.threads) * (rows + kGradStages * 8),
                                groups * a.c * 8);
-  constexpr auto kernel = norm_grad_row_kernel<T, E, V, ACT, WIDE>;
+  constexpr auto kernel = norm_grad_row_kernel<T, E, V, ACT, LANES>;
   cudaError_t e = allow_smem<kernel>(smem);
   if (e != cudaSuccess) return e;
   const int64_t blocks = blocks_for(p, a.n, kGradThreads, num_sms, layer_norm_chunks(a.n));
@@ -831,13 +879,17 @@ cudaError_t launch_grad_rows(const LayerNormGradArgs& a, const RowPlan& p, int n
                     static_cast<int>(blocks), a.c, a.dweight, a.dbias);
 }
 
-// f<T, E, V, ACT, WIDE> of a plan.
-#define SUBM3D_ROW_WIDE(f, T, E, V, ACT, p, ...) \
-  ((p).lanes > 32 ? f<T, E, V, ACT, true>(__VA_ARGS__) : f<T, E, V, ACT, false>(__VA_ARGS__))
+// f<T, E, V, ACT, LANES> of a plan (LANES 0: teams of several warps).
+#define SUBM3D_ROW_LANES(f, T, E, V, ACT, p, ...)                   \
+  ((p).lanes > 32    ? f<T, E, V, ACT, 0>(__VA_ARGS__)              \
+   : (p).lanes == 32 ? f<T, E, V, ACT, 32>(__VA_ARGS__)             \
+   : (p).lanes == 16 ? f<T, E, V, ACT, 16>(__VA_ARGS__)             \
+   : (p).lanes == 8  ? f<T, E, V, ACT, 8>(__VA_ARGS__)              \
+                     : f<T, E, V, ACT, kFewestLanes>(__VA_ARGS__))
 #define SUBM3D_ROW_ACT(f, T, E, V, act, p, ...)                                        \
-  ((act) == kActGelu ? SUBM3D_ROW_WIDE(f, T, E, V, kActGelu, p, __VA_ARGS__)           \
-                     : ((act) == kActSilu ? SUBM3D_ROW_WIDE(f, T, E, V, kActSilu, p, __VA_ARGS__) \
-                                          : SUBM3D_ROW_WIDE(f, T, E, V, kActNone, p, __VA_ARGS__)))
+  ((act) == kActGelu ? SUBM3D_ROW_LANES(f, T, E, V, kActGelu, p, __VA_ARGS__)           \
+                     : ((act) == kActSilu ? SUBM3D_ROW_LANES(f, T, E, V, kActSilu, p, __VA_ARGS__) \
+                                          : SUBM3D_ROW_LANES(f, T, E, V, kActNone, p, __VA_ARGS__)))
 #define SUBM3D_ROW_PLAN(f, a, p, ...)                                                         \
   ((a).bf16 ? ((p).vec == 8 ? SUBM3D_ROW_ACT(f, __nv_bfloat16, 8, 2, (a).act, p, __VA_ARGS__) \
                : (p).vec == 2 ? SUBM3D_ROW_ACT(f, __nv_bfloat16, 2, 8, (a).act, p, __VA_ARGS__) \
@@ -847,10 +899,13 @@ cudaError_t launch_grad_rows(const LayerNormGradArgs& a, const RowPlan& p, int n
 
 }  // namespace
 
-cudaError_t launch_layer_norm(const LayerNormArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_layer_norm(const LayerNormArgs& in, int num_sms, cudaStream_t stream) {
+  LayerNormArgs a = in;
   const int align = std::min(rows_align(a.x, a.x_stride, a.bf16), rows_align(a.y, a.c, a.bf16));
   const RowPlan p = row_plan(a.c, a.bf16, align, kMaxRowWarps);
-  if (p.lanes > 0) return SUBM3D_ROW_PLAN(launch_norm_rows, a, p, a, p, num_sms, stream);
+  const int64_t row_bytes = a.x_stride * (a.bf16 ? 2 : 4);
+  a.row_bytes = static_cast<uint32_t>(row_bytes);
+  if (p.lanes > 0 && a.n <= kMaxRows && row_bytes <= 0xFFFFFFFFll) return SUBM3D_ROW_PLAN(launch_norm_rows, a, p, a, p, num_sms, stream);
   const dim3 grid(static_cast<unsigned>(std::min(a.n, static_cast<int64_t>(num_sms) * 8)));
   return a.bf16 ? launch_pdl(norm_any_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, stream, a)
                 : launch_pdl(norm_any_kernel<float>, grid, dim3(kThreads), 0, stream, a);
@@ -864,7 +919,10 @@ cudaError_t launch_layer_norm_grad(const LayerNormGradArgs& in, int num_sms, cud
                               rows_align(a.dy, a.dy_stride, a.bf16),
                               rows_align(a.dx, a.c, a.bf16)});
   const RowPlan p = row_plan(a.c, a.bf16, align, kMaxGradWarps);
-  if (p.lanes > 0) return SUBM3D_ROW_PLAN(launch_grad_rows, a, p, a, p, num_sms, stream);
+  const int64_t x_bytes = a.x_stride * (a.bf16 ? 2 : 4), dy_bytes = a.dy_stride * (a.bf16 ? 2 : 4);
+  a.x_row_bytes = static_cast<uint32_t>(x_bytes);
+  a.dy_row_bytes = static_cast<uint32_t>(dy_bytes);
+  if (p.lanes > 0 && a.n <= kMaxRows && std::max(x_bytes, dy_bytes) <= 0xFFFFFFFFll) return SUBM3D_ROW_PLAN(launch_grad_rows, a, p, a, p, num_sms, stream);
   if (a.dx) {
     const int64_t blocks = std::min(a.n, static_cast<int64_t>(num_sms) * 8);
     const dim3 grid(static_cast<unsigned>(blocks));
