@@ -245,7 +245,9 @@ __global__ void __launch_bounds__(kThreads) norm_dw_join_kernel(const float* par
 #define KS 4
 #define KG 3
 #endif
-constexpr int kRowStages = KS, kGradStages = KG;
+constexpr int kRowStages = KS;
+template <typename T, int E, int V>
+constexpr int kGradStages = sizeof(T) * E * V >= 64 ? 2 : KG;
 constexpr int kMaxRowWarps = 16;  // forward: rows up to 16 * 32 * 16 = 8,192 elements
 constexpr int kMaxGradWarps = 8;  // backward: 4,096
 // Rows are counted in 32 bits, some strides of all teams beyond the last one included.
@@ -370,6 +372,13 @@ __device__ __forceinline__ Team team_of(int lanes) {
   return t;
 }
 
+// v, in a register: not to be computed again at each use (which costs more
+// instructions than the register saves).
+__device__ __forceinline__ uint32_t kept(uint32_t v) {
+  asm volatile("mov.b32 %0, %0;" : "+r"(v));
+  return v;
+}
+
 // A lane's parts of the rows ahead.  Parts of 4, 8 or 16 bytes are copied into the
 // lane's own shared-memory slots (S stages, at byte offsets 0, kStage, ... of a
 // thread's slot); single bf16 elements (odd widths) are held in registers, one row
@@ -389,7 +398,7 @@ struct Ahead {
   static __device__ __forceinline__ uint32_t stage_bytes() { return threads() * V * kBytes; }
 
   __device__ __forceinline__ void init(uint32_t smem, const void* x, const Team& t, int vecs) {
-    mine = smem + threadIdx.x * kBytes;
+    mine = kept(smem + threadIdx.x * kBytes);
     src = static_cast<const char*>(x) + static_cast<int64_t>(t.first) * kBytes;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
@@ -408,36 +417,32 @@ struct Ahead {
       asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + i), "r"(0) : "memory");
   }
   // Starts on row r, into the stage at byte offset `at`; zeros where there is none.
+  // (Predicated copies that fill with zeros: no branch.)
   __device__ __forceinline__ void fetch(uint32_t at, uint32_t r, uint32_t row_bytes, bool live,
                                         const Team& t) {
-    if (live) {
-      const char* row = src + static_cast<uint64_t>(r) * row_bytes;
+    const char* row = src + static_cast<uint64_t>(live ? r : 0u) * row_bytes;
+    const int bytes = live ? kBytes : 0;
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const char* p = row + k * t.step * kBytes;
-        if (!on[k]) continue;
-        if constexpr (!kAsync) {
-          uint16_t h;
-          asm volatile("ld.global.b16 %0, [%1];" : "=h"(h) : "l"(p));
-          held[k] = h;
-        } else {
-          const uint32_t dst = mine + at + k * threads() * kBytes;
-          if constexpr (kBytes == 16)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(p)
-                         : "memory");
-          else
-            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(p),
-                         "n"(kBytes)
-                         : "memory");
-        }
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        if constexpr (kAsync)
-          zero(at, k);
+    for (int k = 0; k < V; ++k) {
+      const char* p = row + k * t.step * kBytes;
+      if constexpr (!kAsync) {
+        uint16_t h = 0;
+        if (live && on[k]) asm volatile("ld.global.b16 %0, [%1];" : "=h"(h) : "l"(p));
+        held[k] = h;
+      } else {
+        const uint32_t dst = mine + at + k * threads() * kBytes;
+        if constexpr (kBytes == 16)
+          asm volatile(
+              "{\n .reg .pred q;\n setp.ne.s32 q, %3, 0;\n"
+              " @q cp.async.cg.shared.global [%0], [%1], 16, %2;\n}" ::"r"(dst),
+              "l"(p), "r"(bytes), "r"(static_cast<int>(on[k]))
+              : "memory");
         else
-          held[k] = 0u;
+          asm volatile(
+              "{\n .reg .pred q;\n setp.ne.s32 q, %4, 0;\n"
+              " @q cp.async.ca.shared.global [%0], [%1], %2, %3;\n}" ::"r"(dst),
+              "l"(p), "n"(kBytes), "r"(bytes), "r"(static_cast<int>(on[k]))
+              : "memory");
       }
     }
   }
@@ -477,28 +482,38 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
 
-// The lane's vectors into its row, p = where its first one goes.
+// The lane's vectors into its row, p = where its first one goes; `live`: there is one.
 template <typename T, int E, int V>
 __device__ __forceinline__ void store_row(T* p, const f2 (&v)[V * E / 2], const bool (&on)[V],
-                                          const Team& t) {
+                                          bool live, const Team& t) {
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    if (!on[k]) continue;
     T* q = p + k * t.step * E;
-    const int j = k * E / 2;
+    const int go = on[k] && live, j = k * E / 2;
     float lo, hi;
     f2_unpack(v[j], lo, hi);
-    if constexpr (sizeof(T) == 2 && E == 8) {
-      *reinterpret_cast<uint4*>(q) = make_uint4(to_bf16_pair(v[j]), to_bf16_pair(v[j + 1]),
-                                                to_bf16_pair(v[j + 2]), to_bf16_pair(v[j + 3]));
-    } else if constexpr (sizeof(T) == 2 && E == 2) {
-      *reinterpret_cast<uint32_t*>(q) = to_bf16_pair(v[j]);
-    } else if constexpr (sizeof(T) == 4 && E == 4) {
-      float l1, h1;
-      f2_unpack(v[j + 1], l1, h1);
-      *reinterpret_cast<float4*>(q) = make_float4(lo, hi, l1, h1);
+    if constexpr (sizeof(T) * E == 16) {
+      uint32_t w[4];
+      if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = to_bf16_pair(v[j + i]);
+      } else {
+        float l1, h1;
+        f2_unpack(v[j + 1], l1, h1);
+        w[0] = __float_as_uint(lo);
+        w[1] = __float_as_uint(hi);
+        w[2] = __float_as_uint(l1);
+        w[3] = __float_as_uint(h1);
+      }
+      asm volatile(
+          "{\n .reg .pred q;\n setp.ne.s32 q, %5, 0;\n"
+          " @q st.global.v4.b32 [%0], {%1, %2, %3, %4};\n}" ::"l"(q),
+          "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(go)
+          : "memory");
+    } else if constexpr (E == 2) {
+      if (go) *reinterpret_cast<uint32_t*>(q) = to_bf16_pair(v[j]);
     } else {
-      *q = from_f32<T>(k % 2 ? hi : lo);
+      if (go) *q = from_f32<T>(k % 2 ? hi : lo);
     }
   }
 }
@@ -625,12 +640,11 @@ __global__ void __launch_bounds__(LANES == 0 ? kMaxRowWarps * 32 : kThreads,
       const f2 d = WIDE ? f2_add(v[i], moved) : v[i];
       v[i] = act_pair<ACT>(f2_fma(f2_mul(d, rs), w[i], b[i]));
     }
-    if (r < n) {
-      store_row<T, E, V>(y + static_cast<uint64_t>(r) * static_cast<uint32_t>(a.c), v, ahead.on, t);
-      if (a.mean && t.leader) {
-        a.mean[r] = mean;
-        a.rstd[r] = rstd;
-      }
+    store_row<T, E, V>(y + static_cast<uint64_t>(r) * static_cast<uint32_t>(a.c), v, ahead.on,
+                       r < n, t);
+    if (a.mean && t.leader && r < n) {
+      a.mean[r] = mean;
+      a.rstd[r] = rstd;
     }
   }
 }
@@ -645,7 +659,7 @@ __global__ void __launch_bounds__(kMaxGradWarps * 32, kGradThreads / (kMaxGradWa
   __shared__ float2 slot[2][WIDE ? kMaxGradWarps : 1];
   extern __shared__ __align__(16) uint8_t ring[];  // rows ahead; at the end the sums
   constexpr int N = V * E;
-  constexpr int S = kGradStages;
+  constexpr int S = kGradStages<T, E, V>;
   pdl_wait();
   const Team t = team_of<V, LANES>(lanes);
   const int vecs = a.c / E;
@@ -657,7 +671,7 @@ __global__ void __launch_bounds__(kMaxGradWarps * 32, kGradThreads / (kMaxGradWa
   ax.init(smem_u32(ring), a.x, t, vecs);
   ay.init(smem_u32(ring) + threads * kRing, a.dy, t, vecs);
   // a row's mean and rstd, fetched with it
-  const uint32_t stats = smem_u32(ring) + threads * 2 * kRing + threadIdx.x * 4;
+  const uint32_t stats = kept(smem_u32(ring) + threads * 2 * kRing + threadIdx.x * 4);
   constexpr uint32_t kRowBytes = A::kAsync ? V * A::kBytes : 8;  // a stage, per thread
   const uint32_t n = static_cast<uint32_t>(a.n);
   // stages are told apart by the byte offset of their rows' slots (single elements,
@@ -667,26 +681,35 @@ __global__ void __launch_bounds__(kMaxGradWarps * 32, kGradThreads / (kMaxGradWa
     const bool live = r < n;
     ax.fetch(at, r, a.x_row_bytes, live, t);
     ay.fetch(at, r, a.dy_row_bytes, live, t);
-    const uint32_t to = stats_at(at);
-    if (live) {
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(a.mean + r)
-                   : "memory");
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + threads * 4),
-                   "l"(a.rstd + r)
-                   : "memory");
-    } else {
-      asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(0) : "memory");
-      asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + threads * 4), "r"(0) : "memory");
-    }
+    const uint32_t to = stats_at(at), row = live ? r : 0u;
+    const int bytes = live ? 4 : 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(a.mean + row),
+                 "r"(bytes)
+                 : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + threads * 4),
+                 "l"(a.rstd + row), "r"(bytes)
+                 : "memory");
     copies_commit();
   };
   const uint32_t stage = threads * kRowBytes;
   const uint32_t last_stage = A::kFront * stage;
 #pragma unroll
   for (int s = 0; s < A::kFront; ++s) fetch(s * stage, t.row + s * t.stride);
-  f2 w[N / 2], b[N / 2], dw[N / 2], db[N / 2];
+  f2 w[N / 2], dw[N / 2], db[N / 2];
   load_affine<E, V>(w, a.weight, a.affine_bf16, 1.0f, t, vecs);
-  if (ACT != kActNone) load_affine<E, V>(b, a.bias, a.affine_bf16, 0.0f, t, vecs);
+  // the bias waits in the lane's slots, 8 bytes a pair of elements: in registers it
+  // would be the sixth array of N
+  uint32_t bias = 0;
+  if (ACT != kActNone) {
+    f2 b[N / 2];
+    load_affine<E, V>(b, a.bias, a.affine_bf16, 0.0f, t, vecs);
+    bias = kept(smem_u32(ring) + threads * (2 * kRing + S * 8) + threadIdx.x * 16);
+#pragma unroll
+    for (int i = 0; i < N / 2; i += 2)
+      asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(bias + i / 2 * threads * 16),
+                   "l"(b[i]), "l"(b[i + 1])
+                   : "memory");
+  }
 #pragma unroll
   for (int i = 0; i < N / 2; ++i) dw[i] = db[i] = f2_set(0.0f);
   T* dx = static_cast<T*>(a.dx) + t.first * E;
@@ -708,10 +731,18 @@ __global__ void __launch_bounds__(kMaxGradWarps * 32, kGradThreads / (kMaxGradWa
     cur = cur == last_stage ? 0 : cur + stage;
     const f2 shift = f2_set(-mean), rs = f2_set(rstd);
     f2 s0 = f2_set(0.0f), s1 = f2_set(0.0f);
+    f2 b[2];
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
       h[i] = f2_mul(f2_add(h[i], shift), rs);
-      if (ACT != kActNone) g[i] = f2_mul(g[i], slope_pair<ACT>(f2_fma(h[i], w[i], b[i])));
+      if (ACT != kActNone) {
+        if (i % 2 == 0)
+          asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
+                       : "=l"(b[0]), "=l"(b[1])
+                       : "r"(bias + i / 2 * threads * 16)
+                       : "memory");
+        g[i] = f2_mul(g[i], slope_pair<ACT>(f2_fma(h[i], w[i], b[i % 2])));
+      }
       db[i] = f2_add(db[i], g[i]);
       dw[i] = f2_fma(g[i], h[i], dw[i]);
       g[i] = f2_mul(g[i], w[i]);
@@ -730,12 +761,11 @@ __global__ void __launch_bounds__(kMaxGradWarps * 32, kGradThreads / (kMaxGradWa
       }
       turn ^= 1;
     }
-    if (r < n && a.dx) {
-      const f2 c0 = f2_set(-m0 * inv_c * rstd), c1 = f2_set(-m1 * inv_c * rstd);
+    const f2 c0 = f2_set(-m0 * inv_c * rstd), c1 = f2_set(-m1 * inv_c * rstd);
 #pragma unroll
-      for (int i = 0; i < N / 2; ++i) g[i] = f2_fma(h[i], c1, f2_fma(g[i], rs, c0));
-      store_row<T, E, V>(dx + static_cast<uint64_t>(r) * static_cast<uint32_t>(a.c), g, ax.on, t);
-    }
+    for (int i = 0; i < N / 2; ++i) g[i] = f2_fma(h[i], c1, f2_fma(g[i], rs, c0));
+    store_row<T, E, V>(dx + static_cast<uint64_t>(r) * static_cast<uint32_t>(a.c), g, ax.on,
+                       r < n && a.dx, t);
   }
   if (!a.partial) return;
   // The lanes with the same columns: first the teams of a warp by shuffles, then the
@@ -862,10 +892,12 @@ cudaError_t launch_norm_rows(const LayerNormArgs& a, const RowPlan& p, int num_s
 template <typename T, int E, int V, int ACT, int LANES>
 cudaError_t launch_grad_rows(const LayerNormGradArgs& a, const RowPlan& p, int num_sms,
                              cudaStream_t stream) {
-  using A = Ahead<T, E, V, kGradStages, 0>;
-  const size_t rows = A::kAsync ? 2 * kGradStages * V * A::kBytes : 0;
+  constexpr int S = kGradStages<T, E, V>;
+  using A = Ahead<T, E, V, S, 0>;
+  const size_t rows = A::kAsync ? 2 * S * V * A::kBytes : 0;
   const size_t groups = LANES == 0 ? p.teams : p.threads / 32;
-  const size_t smem = std::max(static_cast<size_t>(p.threads) * (rows + kGradStages * 8),
+  const size_t bias = ACT != kActNone ? V * E * 4 : 0;
+  const size_t smem = std::max(static_cast<size_t>(p.threads) * (rows + S * 8 + bias),
                                groups * a.c * 8);
   constexpr auto kernel = norm_grad_row_kernel<T, E, V, ACT, LANES>;
   cudaError_t e = allow_smem<kernel>(smem);
