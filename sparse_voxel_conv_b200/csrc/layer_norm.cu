@@ -207,27 +207,44 @@ __global__ void __launch_bounds__(kThreads) norm_dw_any_kernel(LayerNormGradArgs
   }
 }
 
-// dw (blockIdx.y = 0) and db (1): the chunks' partial sums, in a fixed order.
-__global__ void __launch_bounds__(kThreads) norm_dw_join_kernel(const float* partial, int chunks,
-                                                                int32_t channels, float* dw,
-                                                                float* db) {
-  __shared__ float sh[kWarps][33];
+// dw (blockIdx.y = 0) and db (1): the chunks' partial sums, in a fixed order: 32
+// columns a block, its warps take the chunks in turn, eight loads at a time.
+constexpr int kJoinWarps = 32;
+__global__ void __launch_bounds__(kJoinWarps * 32) norm_dw_join_kernel(const float* partial,
+                                                                      int chunks, int32_t channels,
+                                                                      float* dw, float* db) {
+  __shared__ float sh[kJoinWarps][33];
   pdl_wait();
   const int lane = threadIdx.x % 32, ty = threadIdx.x / 32;
   const int c = blockIdx.x * 32 + lane;
   float* out = blockIdx.y == 0 ? dw : db;
   float s = 0.0f;
-  if (out && c < channels)
-    for (int k = ty; k < chunks; k += kWarps)
-      s += partial[(static_cast<int64_t>(k) * 2 + blockIdx.y) * channels + c];
+  if (out && c < channels) {
+    const float* p = partial + static_cast<int64_t>(blockIdx.y) * channels + c;
+    const int64_t step = 2 * static_cast<int64_t>(channels);
+    for (int k = ty; k < chunks; k += 8 * kJoinWarps) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int chunk = k + i * kJoinWarps;
+        v[i] = chunk < chunks ? p[chunk * step] : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[i];
+    }
+  }
   sh[ty][lane] = s;
   __syncthreads();
-  if (ty == 0 && out && c < channels) {
-    float t = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) t += sh[i][lane];
-    out[c] = t;
-  }
+  // lane l of warp w takes warp l's sum of column w
+  const float t = warp_sum(sh[lane][ty]);
+  const int col = blockIdx.x * 32 + ty;
+  if (lane == 0 && out && col < channels) out[col] = t;
+}
+
+cudaError_t launch_join(const LayerNormGradArgs& a, int chunks, cudaStream_t stream) {
+  return launch_pdl(norm_dw_join_kernel, dim3(static_cast<unsigned>((a.c + 31) / 32), 2),
+                    dim3(kJoinWarps * 32), 0, stream, static_cast<const float*>(a.partial), chunks,
+                    a.c, a.dweight, a.dbias);
 }
 
 // ---------------------------------------------------------------- row kernels ----
@@ -248,13 +265,15 @@ __global__ void __launch_bounds__(kThreads) norm_dw_join_kernel(const float* par
 constexpr int kRowStages = KS;
 template <typename T, int E, int V>
 constexpr int kGradStages = sizeof(T) * E * V >= 64 ? 2 : KG;
-constexpr int kMaxRowWarps = 16;  // forward: rows up to 16 * 32 * 16 = 8,192 elements
-constexpr int kMaxGradWarps = 8;  // backward: 4,096
+constexpr int kMaxRowWarps = 16;  // of a team: rows up to 16 * 32 * 16 = 8,192 elements
 // Rows are counted in 32 bits, some strides of all teams beyond the last one included.
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - (1 << 20);
 constexpr int kFewestLanes = 4;   // of a team: 16 bytes of 64 channels a lane and load
 // Resident threads on an SM that the kernels' register bounds allow.
 constexpr int kRowThreads = 768, kWideRowThreads = 512, kGradThreads = 512;
+// A block's: one block of the wide and the gradient kernels fills an SM, so that few
+// partial sums are left to join.
+constexpr int kWideThreads = 512;
 
 using f2 = unsigned long long;  // two fp32 values
 __device__ __forceinline__ f2 f2_set(float v) { return f2_pack(v, v); }
@@ -380,10 +399,9 @@ __device__ __forceinline__ uint32_t kept(uint32_t v) {
 }
 
 // A lane's parts of the rows ahead.  Parts of 4, 8 or 16 bytes are copied into the
-// lane's own shared-memory slots (S stages, at byte offsets 0, kStage, ... of a
-// thread's slot); single bf16 elements (odd widths) are held in registers, one row
-// ahead.  THREADS: the block's, 0 where it is not a constant.
-template <typename T, int E, int V, int S, int THREADS>
+// lane's own shared-memory slots (S stages, kStage bytes apart); single bf16 elements (odd widths) are held in registers, one row
+// ahead.  A warp's slots lie together, [S][V][32] parts.
+template <typename T, int E, int V, int S>
 struct Ahead {
   static constexpr int kBytes = static_cast<int>(sizeof(T)) * E;
   static constexpr bool kAsync = kBytes >= 4;
@@ -394,11 +412,12 @@ struct Ahead {
   uint32_t held[kAsync ? 1 : V];
   bool on[V];        // the vector lies in the row
 
-  static __device__ __forceinline__ uint32_t threads() { return THREADS ? THREADS : blockDim.x; }
-  static __device__ __forceinline__ uint32_t stage_bytes() { return threads() * V * kBytes; }
+  static constexpr uint32_t kStage = kAsync ? 32 * V * kBytes : 0;
+  static constexpr uint32_t kWarp = S * kStage;  // bytes of a warp
 
+  // smem: the warp's slots
   __device__ __forceinline__ void init(uint32_t smem, const void* x, const Team& t, int vecs) {
-    mine = kept(smem + threadIdx.x * kBytes);
+    mine = kept(smem + threadIdx.x % 32 * kBytes);
     src = static_cast<const char*>(x) + static_cast<int64_t>(t.first) * kBytes;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
@@ -406,12 +425,12 @@ struct Ahead {
       if (!on[k]) {  // columns behind the row's end are zeros for good
         held[kAsync ? 0 : k] = 0u;
         if constexpr (kAsync)
-          for (int s = 0; s < S; ++s) zero(s * stage_bytes(), k);
+          for (int s = 0; s < S; ++s) zero(s * kStage, k);
       }
     }
   }
   __device__ __forceinline__ void zero(uint32_t at, int k) {
-    const uint32_t dst = mine + at + k * threads() * kBytes;
+    const uint32_t dst = mine + at + k * 32 * kBytes;
 #pragma unroll
     for (int i = 0; i < kBytes; i += 4)
       asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + i), "r"(0) : "memory");
@@ -430,7 +449,7 @@ struct Ahead {
         if (live && on[k]) asm volatile("ld.global.b16 %0, [%1];" : "=h"(h) : "l"(p));
         held[k] = h;
       } else {
-        const uint32_t dst = mine + at + k * threads() * kBytes;
+        const uint32_t dst = mine + at + k * 32 * kBytes;
         if constexpr (kBytes == 16)
           asm volatile(
               "{\n .reg .pred q;\n setp.ne.s32 q, %3, 0;\n"
@@ -451,7 +470,7 @@ struct Ahead {
     if constexpr (kAsync) {
 #pragma unroll
       for (int k = 0; k < V; ++k) {
-        const uint32_t from = mine + at + k * threads() * kBytes;
+        const uint32_t from = mine + at + k * 32 * kBytes;
         uint32_t* o = w + k * kBytes / 4;
         if constexpr (kBytes == 16)
           asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -549,7 +568,7 @@ __device__ __forceinline__ void load_affine(f2 (&w)[V * E / 2], const void* p, b
 }
 
 template <typename T, int E, int V, int ACT, int LANES>
-__global__ void __launch_bounds__(LANES == 0 ? kMaxRowWarps * 32 : kThreads,
+__global__ void __launch_bounds__(LANES == 0 ? kWideThreads : kThreads,
                                   LANES == 0 ? 1 : kRowThreads / kThreads)
     norm_row_kernel(LayerNormArgs a, int team_lanes) {
   constexpr bool WIDE = LANES == 0;
@@ -569,15 +588,15 @@ __global__ void __launch_bounds__(LANES == 0 ? kMaxRowWarps * 32 : kThreads,
   const float last_count = static_cast<float>(a.c - (t.warps - 1) * 32 * N);
   const float my_count = t.warp + 1 < t.warps ? 32.0f * N : last_count;
   const float inv_mine = 1.0f / my_count, inv_last = 1.0f / last_count;
-  using A = Ahead<T, E, V, S, WIDE ? 0 : kThreads>;
+  using A = Ahead<T, E, V, S>;
   A ahead;
-  ahead.init(smem_u32(ring), a.x, t, vecs);
+  ahead.init(smem_u32(ring) + threadIdx.x / 32 * A::kWarp, a.x, t, vecs);
   const uint32_t n = static_cast<uint32_t>(a.n);
   const auto fetch = [&](uint32_t at, uint32_t r) {
     ahead.fetch(at, r, a.row_bytes, r < n, t);
     if constexpr (A::kAsync) copies_commit();
   };
-  const uint32_t stage = A::stage_bytes(), last_stage = (S - 1) * stage;
+  constexpr uint32_t stage = A::kStage, last_stage = (S - 1) * stage;
 #pragma unroll
   for (int s = 0; s < A::kFront; ++s) fetch(s * stage, t.row + s * t.stride);
   f2 w[N / 2], b[N / 2];
@@ -620,15 +639,21 @@ __global__ void __launch_bounds__(LANES == 0 ? kMaxRowWarps * 32 : kThreads,
       if (threadIdx.x % 32 == 0) slot[turn][first + t.warp] = make_float2(sum, sq);
       team_barrier(t);
       float whole = 0.0f;
-      for (int i = 0; i < t.warps; ++i) whole += slot[turn][first + i].x;
-      whole *= inv_c;
       sq = 0.0f;
-      for (int i = 0; i < t.warps; ++i) {
-        const float2 e = slot[turn][first + i];
-        const bool end = i + 1 == t.warps;
-        const float d = __fmaf_rn(e.x, end ? inv_last : 1.0f / (32 * N), -whole);
-        sq += __fmaf_rn(d * d, end ? last_count : 32.0f * N, e.y);
-      }
+      for (int i = 0; i < t.warps; i += 4)  // four loads at a time
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (i + j < t.warps) whole += slot[turn][first + i + j].x;
+      whole *= inv_c;
+      for (int i = 0; i < t.warps; i += 4)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (i + j < t.warps) {
+            const float2 e = slot[turn][first + i + j];
+            const bool end = i + j + 1 == t.warps;
+            const float d = __fmaf_rn(e.x, end ? inv_last : 1.0f / (32 * N), -whole);
+            sq += __fmaf_rn(d * d, end ? last_count : 32.0f * N, e.y);
+          }
       turn ^= 1;
       moved = f2_set(mean - whole);
       mean = whole;
@@ -649,14 +674,21 @@ __global__ void __launch_bounds__(LANES == 0 ? kMaxRowWarps * 32 : kThreads,
   }
 }
 
+// Shared memory of a warp of the gradient kernel.
+template <typename T, int E, int V, int ACT>
+__host__ __device__ constexpr uint32_t grad_warp_bytes() {
+  constexpr int S = kGradStages<T, E, V>;
+  return 2 * Ahead<T, E, V, S>::kWarp + S * 256 + (ACT != kActNone ? V * E * 128 : 0);
+}
+
 // dx of the team's rows, and the block's column sums of dz xhat and dz into
 // partial[block][2][C] (or straight into dweight and dbias, for a grid of one).
 template <typename T, int E, int V, int ACT, int LANES>
-__global__ void __launch_bounds__(kMaxGradWarps * 32, kGradThreads / (kMaxGradWarps * 32))
+__global__ void __launch_bounds__(kWideThreads, 1)
     norm_grad_row_kernel(LayerNormGradArgs a, int team_lanes) {
   constexpr bool WIDE = LANES == 0;
   const int lanes = WIDE ? team_lanes : LANES;
-  __shared__ float2 slot[2][WIDE ? kMaxGradWarps : 1];
+  __shared__ float2 slot[2][WIDE ? kMaxRowWarps : 1];
   extern __shared__ __align__(16) uint8_t ring[];  // rows ahead; at the end the sums
   constexpr int N = V * E;
   constexpr int S = kGradStages<T, E, V>;
@@ -664,19 +696,21 @@ __global__ void __launch_bounds__(kMaxGradWarps * 32, kGradThreads / (kMaxGradWa
   const Team t = team_of<V, LANES>(lanes);
   const int vecs = a.c / E;
   const float inv_c = 1.0f / static_cast<float>(a.c);
-  using A = Ahead<T, E, V, S, WIDE ? 0 : kThreads>;
+  using A = Ahead<T, E, V, S>;
   A ax, ay;
-  constexpr int kRing = A::kAsync ? S * V * A::kBytes : 0;  // bytes a thread
-  const uint32_t threads = A::threads();
-  ax.init(smem_u32(ring), a.x, t, vecs);
-  ay.init(smem_u32(ring) + threads * kRing, a.dy, t, vecs);
-  // a row's mean and rstd, fetched with it
-  const uint32_t stats = kept(smem_u32(ring) + threads * 2 * kRing + threadIdx.x * 4);
-  constexpr uint32_t kRowBytes = A::kAsync ? V * A::kBytes : 8;  // a stage, per thread
+  // a warp's part: the two rows' slots, a row's mean and rstd [S][2][32], the bias
+  constexpr uint32_t kStats = 2 * A::kWarp, kBias = kStats + S * 256;
+  const uint32_t warp_part =
+      smem_u32(ring) + threadIdx.x / 32 * grad_warp_bytes<T, E, V, ACT>();
+  ax.init(warp_part, a.x, t, vecs);
+  ay.init(warp_part + A::kWarp, a.dy, t, vecs);
+  const uint32_t stats = kept(warp_part + kStats + threadIdx.x % 32 * 4);
+  constexpr uint32_t stage = A::kAsync ? A::kStage : 256;
+  constexpr uint32_t last_stage = A::kFront * stage;
   const uint32_t n = static_cast<uint32_t>(a.n);
   // stages are told apart by the byte offset of their rows' slots (single elements,
   // which are not copied: by that of their statistics)
-  const auto stats_at = [&](uint32_t at) { return stats + at / kRowBytes * 8; };
+  const auto stats_at = [&](uint32_t at) { return stats + at / stage * 256; };
   const auto fetch = [&](uint32_t at, uint32_t r) {
     const bool live = r < n;
     ax.fetch(at, r, a.x_row_bytes, live, t);
@@ -686,13 +720,11 @@ __global__ void __launch_bounds__(kMaxGradWarps * 32, kGradThreads / (kMaxGradWa
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(a.mean + row),
                  "r"(bytes)
                  : "memory");
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + threads * 4),
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + 128),
                  "l"(a.rstd + row), "r"(bytes)
                  : "memory");
     copies_commit();
   };
-  const uint32_t stage = threads * kRowBytes;
-  const uint32_t last_stage = A::kFront * stage;
 #pragma unroll
   for (int s = 0; s < A::kFront; ++s) fetch(s * stage, t.row + s * t.stride);
   f2 w[N / 2], dw[N / 2], db[N / 2];
@@ -703,10 +735,10 @@ __global__ void __launch_bounds__(kMaxGradWarps * 32, kGradThreads / (kMaxGradWa
   if (ACT != kActNone) {
     f2 b[N / 2];
     load_affine<E, V>(b, a.bias, a.affine_bf16, 0.0f, t, vecs);
-    bias = kept(smem_u32(ring) + threads * (2 * kRing + S * 8) + threadIdx.x * 16);
+    bias = kept(warp_part + kBias + threadIdx.x % 32 * 16);
 #pragma unroll
     for (int i = 0; i < N / 2; i += 2)
-      asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(bias + i / 2 * threads * 16),
+      asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(bias + i / 2 * 512),
                    "l"(b[i]), "l"(b[i + 1])
                    : "memory");
   }
@@ -724,7 +756,7 @@ __global__ void __launch_bounds__(kMaxGradWarps * 32, kGradThreads / (kMaxGradWa
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(mean) : "r"(stats_at(cur)) : "memory");
     asm volatile("ld.shared.f32 %0, [%1];"
                  : "=f"(rstd)
-                 : "r"(stats_at(cur) + threads * 4)
+                 : "r"(stats_at(cur) + 128)
                  : "memory");
     fetch(freed, r + A::kFront * t.stride);
     freed = cur;
@@ -739,7 +771,7 @@ __global__ void __launch_bounds__(kMaxGradWarps * 32, kGradThreads / (kMaxGradWa
         if (i % 2 == 0)
           asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
                        : "=l"(b[0]), "=l"(b[1])
-                       : "r"(bias + i / 2 * threads * 16)
+                       : "r"(bias + i / 2 * 512)
                        : "memory");
         g[i] = f2_mul(g[i], slope_pair<ACT>(f2_fma(h[i], w[i], b[i % 2])));
       }
@@ -755,10 +787,14 @@ __global__ void __launch_bounds__(kMaxGradWarps * 32, kGradThreads / (kMaxGradWa
       if (threadIdx.x % 32 == 0) slot[turn][first + t.warp] = make_float2(m0, m1);
       team_barrier(t);
       m0 = m1 = 0.0f;
-      for (int i = 0; i < t.warps; ++i) {
-        m0 += slot[turn][first + i].x;
-        m1 += slot[turn][first + i].y;
-      }
+      for (int i = 0; i < t.warps; i += 4)  // four loads at a time
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (i + j < t.warps) {
+            const float2 e = slot[turn][first + i + j];
+            m0 += e.x;
+            m1 += e.y;
+          }
       turn ^= 1;
     }
     const f2 c0 = f2_set(-m0 * inv_c * rstd), c1 = f2_set(-m1 * inv_c * rstd);
@@ -818,14 +854,12 @@ struct RowPlan {
   int vec = 0;    // elements a load
   int v = 0;      // loads a lane
   int lanes = 0;  // threads of a team; 0: the row is too wide
-  int threads = 0;
-  int64_t teams = 0;  // of a block
 };
 
 // Loads of 16 bytes where the rows' starts and widths are multiples of that, else of
 // 4 where they are (bf16), else of an element.  A lane holds 16 elements (8 single
 // ones); teams are as small as that allows.
-RowPlan row_plan(int32_t c, bool bf16, int align, int max_warps) {
+RowPlan row_plan(int32_t c, bool bf16, int align) {
   RowPlan p;
   p.vec = align == 16 ? (bf16 ? 8 : 4) : (align == 4 && bf16 ? 2 : 1);
   p.v = p.vec > 1 ? 16 / p.vec : 8;
@@ -833,23 +867,29 @@ RowPlan row_plan(int32_t c, bool bf16, int align, int max_warps) {
   if (vecs <= 32 * p.v) {
     p.lanes = kFewestLanes;
     while (p.lanes * p.v < vecs) p.lanes *= 2;
-    p.threads = kThreads;
   } else {
     const int warps = (vecs + 32 * p.v - 1) / (32 * p.v);
-    if (warps > max_warps) return p;
-    p.lanes = warps * 32;
-    const int teams = warps < 8 ? 8 / warps : 1;
-    p.threads = teams * p.lanes;
+    if (warps <= kMaxRowWarps) p.lanes = warps * 32;
   }
-  p.teams = p.threads / p.lanes;
   return p;
+}
+
+// Threads of a block: whole teams, up to `most`; fewer where there would be fewer
+// blocks than SMs, down to four warps.
+int block_threads(int lanes, int64_t n, int most, int num_sms) {
+  const int unit = std::max(lanes, 32);
+  int threads = most / unit * unit;
+  while (threads >= 2 * unit && threads > 128 && threads / lanes * static_cast<int64_t>(num_sms) > n)
+    threads = threads / 2 / unit * unit;
+  return threads;
 }
 
 // Blocks for n rows: as many as there are teams for, up to what fits on the device
 // at once (teams walk on from there) and `most`.
-int64_t blocks_for(const RowPlan& p, int64_t n, int sm_threads, int num_sms, int64_t most) {
-  const int64_t resident = static_cast<int64_t>(std::max(1, sm_threads / p.threads)) * num_sms;
-  return std::min({(n + p.teams - 1) / p.teams, resident, most});
+int64_t blocks_for(int lanes, int threads, int64_t n, int sm_threads, int num_sms, int64_t most) {
+  const int64_t teams = threads / lanes;
+  const int64_t resident = static_cast<int64_t>(std::max(1, sm_threads / threads)) * num_sms;
+  return std::min({(n + teams - 1) / teams, resident, most});
 }
 
 // The largest of 16, 4 and the element's bytes that every row's start is a multiple of.
@@ -869,7 +909,7 @@ cudaError_t allow_smem(size_t bytes) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = uint64_t(1) << (dev & 63);
   if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
-  e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+  e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
   if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_release);
   return e;
 }
@@ -877,14 +917,15 @@ cudaError_t allow_smem(size_t bytes) {
 template <typename T, int E, int V, int ACT, int LANES>
 cudaError_t launch_norm_rows(const LayerNormArgs& a, const RowPlan& p, int num_sms,
                              cudaStream_t stream) {
-  using A = Ahead<T, E, V, kRowStages, 0>;
-  const size_t smem = A::kAsync ? static_cast<size_t>(p.threads) * kRowStages * V * A::kBytes : 0;
+  const int threads = block_threads(p.lanes, a.n, LANES == 0 ? kWideThreads : kThreads, num_sms);
+  const size_t smem = threads / 32 * Ahead<T, E, V, kRowStages>::kWarp;
   constexpr auto kernel = norm_row_kernel<T, E, V, ACT, LANES>;
   const cudaError_t e = allow_smem<kernel>(smem);
   if (e != cudaSuccess) return e;
-  const int64_t blocks =
-      blocks_for(p, a.n, LANES == 0 ? kWideRowThreads : kRowThreads, num_sms, 0x7FFFFFFF);
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(p.threads), smem, stream, a,
+  const int64_t blocks = blocks_for(p.lanes, threads, a.n,
+                                    LANES == 0 ? kWideRowThreads : kRowThreads, num_sms,
+                                    0x7FFFFFFF);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(threads), smem, stream, a,
                     p.lanes);
 }
 
@@ -892,23 +933,19 @@ cudaError_t launch_norm_rows(const LayerNormArgs& a, const RowPlan& p, int num_s
 template <typename T, int E, int V, int ACT, int LANES>
 cudaError_t launch_grad_rows(const LayerNormGradArgs& a, const RowPlan& p, int num_sms,
                              cudaStream_t stream) {
-  constexpr int S = kGradStages<T, E, V>;
-  using A = Ahead<T, E, V, S, 0>;
-  const size_t rows = A::kAsync ? 2 * S * V * A::kBytes : 0;
-  const size_t groups = LANES == 0 ? p.teams : p.threads / 32;
-  const size_t bias = ACT != kActNone ? V * E * 4 : 0;
-  const size_t smem = std::max(static_cast<size_t>(p.threads) * (rows + S * 8 + bias),
-                               groups * a.c * 8);
+  const int threads = block_threads(p.lanes, a.n, kWideThreads, num_sms);
+  const size_t groups = LANES == 0 ? threads / p.lanes : threads / 32;
+  const size_t smem =
+      std::max<size_t>(threads / 32 * grad_warp_bytes<T, E, V, ACT>(), groups * a.c * 8);
   constexpr auto kernel = norm_grad_row_kernel<T, E, V, ACT, LANES>;
   cudaError_t e = allow_smem<kernel>(smem);
   if (e != cudaSuccess) return e;
-  const int64_t blocks = blocks_for(p, a.n, kGradThreads, num_sms, layer_norm_chunks(a.n));
-  e = launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(p.threads), smem, stream, a,
+  const int64_t blocks =
+      blocks_for(p.lanes, threads, a.n, kGradThreads, num_sms, layer_norm_chunks(a.n));
+  e = launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(threads), smem, stream, a,
                  p.lanes);
   if (e != cudaSuccess || !a.partial || blocks == 1) return e;
-  return launch_pdl(norm_dw_join_kernel, dim3(static_cast<unsigned>((a.c + 31) / 32), 2),
-                    dim3(kThreads), 0, stream, static_cast<const float*>(a.partial),
-                    static_cast<int>(blocks), a.c, a.dweight, a.dbias);
+  return launch_join(a, static_cast<int>(blocks), stream);
 }
 
 // f<T, E, V, ACT, LANES> of a plan (LANES 0: teams of several warps).
@@ -934,7 +971,7 @@ cudaError_t launch_grad_rows(const LayerNormGradArgs& a, const RowPlan& p, int n
 cudaError_t launch_layer_norm(const LayerNormArgs& in, int num_sms, cudaStream_t stream) {
   LayerNormArgs a = in;
   const int align = std::min(rows_align(a.x, a.x_stride, a.bf16), rows_align(a.y, a.c, a.bf16));
-  const RowPlan p = row_plan(a.c, a.bf16, align, kMaxRowWarps);
+  const RowPlan p = row_plan(a.c, a.bf16, align);
   const int64_t row_bytes = a.x_stride * (a.bf16 ? 2 : 4);
   a.row_bytes = static_cast<uint32_t>(row_bytes);
   if (p.lanes > 0 && a.n <= kMaxRows && row_bytes <= 0xFFFFFFFFll) return SUBM3D_ROW_PLAN(launch_norm_rows, a, p, a, p, num_sms, stream);
@@ -950,7 +987,7 @@ cudaError_t launch_layer_norm_grad(const LayerNormGradArgs& in, int num_sms, cud
   const int align = std::min({rows_align(a.x, a.x_stride, a.bf16),
                               rows_align(a.dy, a.dy_stride, a.bf16),
                               rows_align(a.dx, a.c, a.bf16)});
-  const RowPlan p = row_plan(a.c, a.bf16, align, kMaxGradWarps);
+  const RowPlan p = row_plan(a.c, a.bf16, align);
   const int64_t x_bytes = a.x_stride * (a.bf16 ? 2 : 4), dy_bytes = a.dy_stride * (a.bf16 ? 2 : 4);
   a.x_row_bytes = static_cast<uint32_t>(x_bytes);
   a.dy_row_bytes = static_cast<uint32_t>(dy_bytes);
@@ -971,9 +1008,7 @@ cudaError_t launch_layer_norm_grad(const LayerNormGradArgs& in, int num_sms, cud
                           rows)
              : launch_pdl(norm_dw_any_kernel<float>, grid, dim3(kThreads), 0, stream, a, rows);
   if (e != cudaSuccess) return e;
-  return launch_pdl(norm_dw_join_kernel, dim3(cols, 2), dim3(kThreads), 0, stream,
-                    static_cast<const float*>(a.partial), static_cast<int>(chunks), a.c,
-                    a.dweight, a.dbias);
+  return launch_join(a, static_cast<int>(chunks), stream);
 }
 
 }  // namespace subm3d
