@@ -292,6 +292,7 @@ struct RotaryArgs {
   const void* pos = nullptr;
   int64_t n = 0, x_row = 0, x_head = 0, y_row = 0, y_head = 0, pos_stride = 0;
   int32_t heads = 0, head_dim = 0, axes = 0, pairs = 0;  // pairs: of all axes
+  int32_t run_heads = 0, runs = 0;  // heads a thread takes, runs of them (set by the launch)
   int32_t axis_pairs[kRotaryMaxAxes] = {};
   bool bf16 = false, pos_f32 = false, halves = false, inverse = false;
   double turns[kRotaryMaxPairs] = {};
@@ -308,6 +309,7 @@ struct AdamWTensor {
   uint8_t* exp_avg_sq_scale;
   float* master;
   int64_t n;
+  bool whole;  // all pointers lie on 16 bytes (codes on 8)
 };
 struct AdamWStep {
   float beta1, one_beta1, beta2, one_beta2, eps;
@@ -325,7 +327,7 @@ struct AdamWList {
   uint32_t first_block[CAP];
   int32_t count, first_tensor;
 };
-constexpr int kAdamWFew = 24, kAdamWMany = 440;
+constexpr int kAdamWFew = 24, kAdamWMany = 400;  // 1.9 KB and 30 KB of parameters
 int64_t adamw_chunk();  // elements a block takes
 template <int CAP>
 cudaError_t launch_adamw(const AdamWStep& a, const AdamWList<CAP>& l, uint32_t blocks, bool bits8,

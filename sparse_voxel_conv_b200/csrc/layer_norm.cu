@@ -249,31 +249,30 @@ cudaError_t launch_join(const LayerNormGradArgs& a, int chunks, cudaStream_t str
 
 // ---------------------------------------------------------------- row kernels ----
 //
-// A team works on one row: 2^k lanes of a warp, or several whole warps (WIDE; LANES = 0).  A
-// lane holds N = V x E elements of the row: V loads of E elements, as wide as the
-// rows' alignment allows.  The row is read once; its sums go over the team by
-// shuffles, and between warps through one exchange in shared memory.  Teams walk
-// over the rows with their columns' weights in registers.  Each lane copies its
-// own part of the rows ahead into its own shared-memory slots (cp.async, kStages
-// deep): no barrier, and the bytes in flight do not cost registers, which are what
-// limits the warps on an SM.
+// A team works on one row: 2^k lanes of a warp, or several whole warps (WIDE;
+// LANES = 0).  A lane holds N = V x E elements of the row: V loads of E elements, as
+// wide as the rows' alignment allows.  The row is read once; its sums go over the
+// team by shuffles, and between warps through one exchange in shared memory.  Teams
+// walk over the rows with their columns' weights in registers.  Each lane copies its
+// own part of the rows ahead into its own shared-memory slots (cp.async): no
+// barrier, and the bytes in flight do not cost registers, which are what limits the
+// warps on an SM.
 
-#ifndef KS
-#define KS 4
-#define KG 3
-#endif
-constexpr int kRowStages = KS;
+// Rows a lane has under way, its present one included.  More cost shared memory and
+// gain nothing (gradient at 329,839 x 128 bf16: 43.3 us with 3, 44.3 with 4); 64-byte
+// parts (fp32) have room for 2.
+constexpr int kRowStages = 4;
 template <typename T, int E, int V>
-constexpr int kGradStages = sizeof(T) * E * V >= 64 ? 2 : KG;
+constexpr int kGradStages = sizeof(T) * E * V >= 64 ? 2 : 3;
 constexpr int kMaxRowWarps = 16;  // of a team: rows up to 16 * 32 * 16 = 8,192 elements
 // Rows are counted in 32 bits, some strides of all teams beyond the last one included.
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - (1 << 20);
 constexpr int kFewestLanes = 4;   // of a team: 16 bytes of 64 channels a lane and load
-// Resident threads on an SM that the kernels' register bounds allow.
-constexpr int kRowThreads = 768, kWideRowThreads = 512, kGradThreads = 512;
-// A block's: one block of the wide and the gradient kernels fills an SM, so that few
-// partial sums are left to join.
-constexpr int kWideThreads = 512;
+// Registers: 80 a thread forward (768 threads an SM), 128 for the gradients (512).  A
+// forward block has up to 256 threads, or one wider team; the gradient's blocks fill an
+// SM each, so that few partial sums are left to join.
+constexpr int kRowRegisters = 80, kRowThreads = 768, kRowBlock = 256;
+constexpr int kGradThreads = 512;
 
 using f2 = unsigned long long;  // two fp32 values
 __device__ __forceinline__ f2 f2_set(float v) { return f2_pack(v, v); }
@@ -398,9 +397,10 @@ __device__ __forceinline__ uint32_t kept(uint32_t v) {
   return v;
 }
 
-// A lane's parts of the rows ahead.  Parts of 4, 8 or 16 bytes are copied into the
-// lane's own shared-memory slots (S stages, kStage bytes apart); single bf16 elements (odd widths) are held in registers, one row
-// ahead.  A warp's slots lie together, [S][V][32] parts.
+// A lane's parts of the rows ahead.  Parts of 4 or 16 bytes are copied into the
+// lane's own shared-memory slots (S stages, kStage bytes apart; a warp's slots lie
+// together, [S][V][32] parts); single bf16 elements (odd widths) are held in
+// registers, one row ahead.
 template <typename T, int E, int V, int S>
 struct Ahead {
   static constexpr int kBytes = static_cast<int>(sizeof(T)) * E;
@@ -568,9 +568,7 @@ __device__ __forceinline__ void load_affine(f2 (&w)[V * E / 2], const void* p, b
 }
 
 template <typename T, int E, int V, int ACT, int LANES>
-__global__ void __launch_bounds__(LANES == 0 ? kWideThreads : kThreads,
-                                  LANES == 0 ? 1 : kRowThreads / kThreads)
-    norm_row_kernel(LayerNormArgs a, int team_lanes) {
+__global__ void __maxnreg__(kRowRegisters) norm_row_kernel(LayerNormArgs a, int team_lanes) {
   constexpr bool WIDE = LANES == 0;
   const int lanes = WIDE ? team_lanes : LANES;
   // warps' sums and squares, two buffers in turn: one is written again only behind the
@@ -640,20 +638,14 @@ __global__ void __launch_bounds__(LANES == 0 ? kWideThreads : kThreads,
       team_barrier(t);
       float whole = 0.0f;
       sq = 0.0f;
-      for (int i = 0; i < t.warps; i += 4)  // four loads at a time
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (i + j < t.warps) whole += slot[turn][first + i + j].x;
+      for (int i = 0; i < t.warps; ++i) whole += slot[turn][first + i].x;
       whole *= inv_c;
-      for (int i = 0; i < t.warps; i += 4)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (i + j < t.warps) {
-            const float2 e = slot[turn][first + i + j];
-            const bool end = i + j + 1 == t.warps;
-            const float d = __fmaf_rn(e.x, end ? inv_last : 1.0f / (32 * N), -whole);
-            sq += __fmaf_rn(d * d, end ? last_count : 32.0f * N, e.y);
-          }
+      for (int i = 0; i < t.warps; ++i) {
+        const float2 e = slot[turn][first + i];
+        const bool end = i + 1 == t.warps;
+        const float d = __fmaf_rn(e.x, end ? inv_last : 1.0f / (32 * N), -whole);
+        sq += __fmaf_rn(d * d, end ? last_count : 32.0f * N, e.y);
+      }
       turn ^= 1;
       moved = f2_set(mean - whole);
       mean = whole;
@@ -684,7 +676,7 @@ __host__ __device__ constexpr uint32_t grad_warp_bytes() {
 // dx of the team's rows, and the block's column sums of dz xhat and dz into
 // partial[block][2][C] (or straight into dweight and dbias, for a grid of one).
 template <typename T, int E, int V, int ACT, int LANES>
-__global__ void __launch_bounds__(kWideThreads, 1)
+__global__ void __launch_bounds__(kGradThreads, 1)
     norm_grad_row_kernel(LayerNormGradArgs a, int team_lanes) {
   constexpr bool WIDE = LANES == 0;
   const int lanes = WIDE ? team_lanes : LANES;
@@ -787,14 +779,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       if (threadIdx.x % 32 == 0) slot[turn][first + t.warp] = make_float2(m0, m1);
       team_barrier(t);
       m0 = m1 = 0.0f;
-      for (int i = 0; i < t.warps; i += 4)  // four loads at a time
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (i + j < t.warps) {
-            const float2 e = slot[turn][first + i + j];
-            m0 += e.x;
-            m1 += e.y;
-          }
+      for (int i = 0; i < t.warps; ++i) {
+        m0 += slot[turn][first + i].x;
+        m1 += slot[turn][first + i].y;
+      }
       turn ^= 1;
     }
     const f2 c0 = f2_set(-m0 * inv_c * rstd), c1 = f2_set(-m1 * inv_c * rstd);
@@ -874,11 +862,11 @@ RowPlan row_plan(int32_t c, bool bf16, int align) {
   return p;
 }
 
-// Threads of a block: whole teams, up to `most`; fewer where there would be fewer
+// Threads of a block: whole teams, up to `most` (or one team); fewer where there would be fewer
 // blocks than SMs, down to four warps.
 int block_threads(int lanes, int64_t n, int most, int num_sms) {
   const int unit = std::max(lanes, 32);
-  int threads = most / unit * unit;
+  int threads = std::max(most / unit, 1) * unit;
   while (threads >= 2 * unit && threads > 128 && threads / lanes * static_cast<int64_t>(num_sms) > n)
     threads = threads / 2 / unit * unit;
   return threads;
@@ -917,14 +905,12 @@ cudaError_t allow_smem(size_t bytes) {
 template <typename T, int E, int V, int ACT, int LANES>
 cudaError_t launch_norm_rows(const LayerNormArgs& a, const RowPlan& p, int num_sms,
                              cudaStream_t stream) {
-  const int threads = block_threads(p.lanes, a.n, LANES == 0 ? kWideThreads : kThreads, num_sms);
+  const int threads = block_threads(p.lanes, a.n, kRowBlock, num_sms);
   const size_t smem = threads / 32 * Ahead<T, E, V, kRowStages>::kWarp;
   constexpr auto kernel = norm_row_kernel<T, E, V, ACT, LANES>;
   const cudaError_t e = allow_smem<kernel>(smem);
   if (e != cudaSuccess) return e;
-  const int64_t blocks = blocks_for(p.lanes, threads, a.n,
-                                    LANES == 0 ? kWideRowThreads : kRowThreads, num_sms,
-                                    0x7FFFFFFF);
+  const int64_t blocks = blocks_for(p.lanes, threads, a.n, kRowThreads, num_sms, 0x7FFFFFFF);
   return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(threads), smem, stream, a,
                     p.lanes);
 }
@@ -933,7 +919,7 @@ cudaError_t launch_norm_rows(const LayerNormArgs& a, const RowPlan& p, int num_s
 template <typename T, int E, int V, int ACT, int LANES>
 cudaError_t launch_grad_rows(const LayerNormGradArgs& a, const RowPlan& p, int num_sms,
                              cudaStream_t stream) {
-  const int threads = block_threads(p.lanes, a.n, kWideThreads, num_sms);
+  const int threads = block_threads(p.lanes, a.n, kGradThreads, num_sms);
   const size_t groups = LANES == 0 ? threads / p.lanes : threads / 32;
   const size_t smem =
       std::max<size_t>(threads / 32 * grad_warp_bytes<T, E, V, ACT>(), groups * a.c * 8);

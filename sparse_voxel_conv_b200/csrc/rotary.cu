@@ -12,8 +12,15 @@
 // it is formed in fp64 and in turns: position * (theta^(-j/n) / 2 pi), minus
 // the nearest whole number (exact); the rest, within [-1/2, 1/2], goes through
 // sincospif.
+//
+// Bound by HBM: x is read and y written once.  A thread takes the P pairs of one
+// 16-byte load (two loads half a vector apart in the halves layout), computes
+// their cos and sin once and keeps them in registers over a run of the row's
+// heads; kUnroll heads are loaded before the first is stored.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+
+#include <algorithm>
 
 #include "internal.h"
 
@@ -21,63 +28,165 @@ namespace subm3d {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kUnroll = 4;
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ void store(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-
-// cos and sin of pair p < a.pairs at row r.
-__device__ __forceinline__ float2 cos_sin(const RotaryArgs& a, int64_t r, int p) {
-  int axis = 0, first = a.axis_pairs[0];
-  while (p >= first) first += a.axis_pairs[++axis];
-  const double pos = a.pos_f32
-                         ? static_cast<double>(static_cast<const float*>(a.pos)[r * a.pos_stride + axis])
-                         : static_cast<double>(static_cast<const int32_t*>(a.pos)[r * a.pos_stride + axis]);
-  const double turns = pos * a.turns[p];
-  const float rest = static_cast<float>(turns - rint(turns));
-  float s, c;
-  sincospif(2.0f * rest, &s, &c);
-  return make_float2(c, a.inverse ? -s : s);
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) {
+  return v;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
 }
 
-// A thread a pair of one head.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) rotary_any_kernel(const __grid_constant__ RotaryArgs a) {
+// E elements of T in one access: 16 bytes, or single ones.
+template <typename T, int E>
+struct Part {
+  T v[E];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (sizeof(T) * E == 16)
+      *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(p);
+    else
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] = p[i];
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (sizeof(T) * E == 16)
+      *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(v);
+    else
+#pragma unroll
+      for (int i = 0; i < E; ++i) p[i] = v[i];
+  }
+};
+
+// cos and sin of P pairs from p0 on at row r; 0 and 0 marks a pair that is copied.
+template <int P>
+__device__ __forceinline__ void cos_sin(const RotaryArgs& a, const double* turns, int64_t r, int p0,
+                                        float (&c)[P], float (&s)[P]) {
+  double pos[kRotaryMaxAxes];
+#pragma unroll
+  for (int i = 0; i < kRotaryMaxAxes; ++i) {
+    pos[i] = 0.0;
+    if (i < a.axes)
+      pos[i] = a.pos_f32 ? static_cast<double>(static_cast<const float*>(a.pos)[r * a.pos_stride + i])
+                         : static_cast<double>(static_cast<const int32_t*>(a.pos)[r * a.pos_stride + i]);
+  }
+  const int e0 = a.axis_pairs[0], e1 = e0 + a.axis_pairs[1], e2 = e1 + a.axis_pairs[2];
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int p = p0 + i;
+    c[i] = s[i] = 0.0f;
+    if (p < a.pairs) {
+      const double at = p < e0 ? pos[0] : (p < e1 ? pos[1] : (p < e2 ? pos[2] : pos[3]));
+      const double t = at * turns[p];
+      sincospif(2.0f * static_cast<float>(t - rint(t)), &s[i], &c[i]);
+      if (a.inverse) s[i] = -s[i];
+    }
+  }
+}
+
+// Items: (row, run of heads, P pairs).  HALVES: the pairs' second elements lie half a
+// vector behind the first ones.
+template <typename T, int P, bool HALVES>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a) {
+  extern __shared__ double turns[];
+  for (int i = threadIdx.x; i < a.pairs; i += kThreads) turns[i] = a.turns[i];
   pdl_wait();
-  const int half = a.head_dim / 2;
-  const int64_t total = a.n * a.heads * half;
+  __syncthreads();
+  constexpr int E = HALVES ? P : 2 * P;
+  const uint32_t half = a.head_dim / 2, slots = half / P, runs = a.runs, run = a.run_heads;
+  const int64_t total = a.n * runs * slots;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
        i += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int p = static_cast<int>(i % half);
-    const int64_t rh = i / half;
-    const int64_t r = rh / a.heads;
-    const int64_t h = rh % a.heads;
-    const T* x = static_cast<const T*>(a.x) + r * a.x_row + h * a.x_head;
-    T* y = static_cast<T*>(a.y) + r * a.y_row + h * a.y_head;
-    const int i0 = a.halves ? p : 2 * p, i1 = a.halves ? p + half : 2 * p + 1;
-    const T x0 = x[i0], x1 = x[i1];
-    if (p >= a.pairs) {
-      y[i0] = x0;
-      y[i1] = x1;
-      continue;
+    int64_t r;
+    uint32_t h0, slot;
+    if (total <= 0xFFFFFFFFll) {
+      const uint32_t j = static_cast<uint32_t>(i), q = j / slots;
+      slot = j - q * slots;
+      const uint32_t row = q / runs;
+      h0 = (q - row * runs) * run;
+      r = row;
+    } else {
+      const int64_t q = i / slots;
+      slot = static_cast<uint32_t>(i - q * slots);
+      r = q / runs;
+      h0 = static_cast<uint32_t>(q - r * runs) * run;
     }
-    const float2 cs = cos_sin(a, r, p);
-    const float f0 = to_f32(x0), f1 = to_f32(x1);
-    store(y + i0, f0 * cs.x - f1 * cs.y);
-    store(y + i1, f0 * cs.y + f1 * cs.x);
+    const uint32_t h1 = min(h0 + run, static_cast<uint32_t>(a.heads));
+    float c[P], s[P];
+    cos_sin<P>(a, turns, r, slot * P, c, s);
+    const T* x = static_cast<const T*>(a.x) + r * a.x_row + slot * E;
+    T* y = static_cast<T*>(a.y) + r * a.y_row + slot * E;
+    for (uint32_t h = h0; h < h1; h += kUnroll) {
+      Part<T, E> lo[kUnroll], hi[HALVES ? kUnroll : 1];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        if (h + u < h1) {
+          lo[u].load(x + (h + u) * a.x_head);
+          if (HALVES) hi[u].load(x + (h + u) * a.x_head + half);
+        }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        if (h + u >= h1) continue;
+        T* first = lo[u].v;
+        T* second = HALVES ? hi[HALVES ? u : 0].v : lo[u].v + 1;
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          T& e0 = first[HALVES ? k : 2 * k];
+          T& e1 = second[HALVES ? k : 2 * k];
+          const float f0 = to_f32(e0), f1 = to_f32(e1);
+          const bool turned = slot * P + k < static_cast<uint32_t>(a.pairs);
+          const T g0 = from_f32<T>(f0 * c[k] - f1 * s[k]), g1 = from_f32<T>(f0 * s[k] + f1 * c[k]);
+          e0 = turned ? g0 : e0;
+          e1 = turned ? g1 : e1;
+        }
+        lo[u].store(y + (h + u) * a.y_head);
+        if (HALVES) hi[HALVES ? u : 0].store(y + (h + u) * a.y_head + half);
+      }
+    }
   }
+}
+
+template <typename T, int P, bool HALVES>
+cudaError_t launch(RotaryArgs a, int num_sms, cudaStream_t stream) {
+  // As many heads in one run as leave every SM its threads (2,048): fewer angles to
+  // compute, but a short call is spread over the device.
+  const int64_t slots = a.head_dim / 2 / P;
+  const int64_t want = static_cast<int64_t>(num_sms) * 2048;
+  const int64_t most_runs = (a.heads + kUnroll - 1) / kUnroll;
+  int64_t runs = std::min(std::max<int64_t>(want / (a.n * slots), 1), most_runs);
+  a.run_heads = static_cast<int32_t>((a.heads + runs - 1) / runs);
+  a.runs = (a.heads + a.run_heads - 1) / a.run_heads;
+  const int64_t total = a.n * a.runs * slots;
+  const int64_t blocks = std::min((total + kThreads - 1) / kThreads,
+                                  static_cast<int64_t>(num_sms) * 64);
+  return launch_pdl(rotary_kernel<T, P, HALVES>, dim3(static_cast<unsigned>(blocks)),
+                    dim3(kThreads), a.pairs * sizeof(double), stream, a);
+}
+
+template <typename T, int WIDE>  // WIDE: elements of 16 bytes
+cudaError_t pick(const RotaryArgs& a, bool vector, int num_sms, cudaStream_t stream) {
+  if (a.halves)
+    return vector && a.head_dim / 2 % WIDE == 0 ? launch<T, WIDE, true>(a, num_sms, stream)
+                                                : launch<T, 1, true>(a, num_sms, stream);
+  return vector && a.head_dim % WIDE == 0 ? launch<T, WIDE / 2, false>(a, num_sms, stream)
+                                          : launch<T, 1, false>(a, num_sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_rotary(const RotaryArgs& a, int num_sms, cudaStream_t stream) {
-  const int64_t total = a.n * a.heads * (a.head_dim / 2);
-  const int64_t want = (total + kThreads - 1) / kThreads;
-  const int64_t most = static_cast<int64_t>(num_sms) * 16;
-  const dim3 grid(static_cast<unsigned>(want < most ? want : most));
-  return a.bf16 ? launch_pdl(rotary_any_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, stream, a)
-                : launch_pdl(rotary_any_kernel<float>, grid, dim3(kThreads), 0, stream, a);
+  const int64_t esz = a.bf16 ? 2 : 4;
+  uintptr_t bits = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y);
+  if (a.n > 1) bits |= static_cast<uintptr_t>((a.x_row | a.y_row) * esz);
+  if (a.heads > 1) bits |= static_cast<uintptr_t>((a.x_head | a.y_head) * esz);
+  const bool vector = bits % 16 == 0;
+  return a.bf16 ? pick<__nv_bfloat16, 8>(a, vector, num_sms, stream)
+                : pick<float, 4>(a, vector, num_sms, stream);
 }
 
 }  // namespace subm3d

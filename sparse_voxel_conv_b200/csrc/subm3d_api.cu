@@ -705,6 +705,9 @@ cudaError_t adamw_lists(const subm3d_adamw_tensor* tensors, int32_t count,
     }
     if (l.count == 0) l.first_tensor = i;
     l.first_block[l.count] = static_cast<uint32_t>(blocks);
+    const size_t state = bits8 ? 8 : 16;
+    const bool whole = aligned(t.param, 16) && aligned(t.grad, 16) && aligned(t.master, 16) &&
+                       aligned(t.exp_avg, state) && aligned(t.exp_avg_sq, state);
     l.tensors[l.count] = {t.param,
                           t.grad,
                           t.exp_avg,
@@ -712,7 +715,8 @@ cudaError_t adamw_lists(const subm3d_adamw_tensor* tensors, int32_t count,
                           static_cast<uint8_t*>(t.exp_avg_scale),
                           static_cast<uint8_t*>(t.exp_avg_sq_scale),
                           static_cast<float*>(t.master),
-                          t.n};
+                          t.n,
+                          whole};
     ++l.count;
     blocks += need;
   }
