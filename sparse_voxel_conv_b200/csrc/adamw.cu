@@ -27,15 +27,24 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include "epilogue.cuh"
 #include "internal.h"
 
 namespace subm3d {
 namespace {
 
+using f2 = unsigned long long;  // two fp32 values
+__device__ __forceinline__ f2 f2_set(float v) { return f2_pack(v, v); }
+
+// A product that keeps its own rounding.  (The assembler joins a mul.f32x2 with the
+// add.f32x2 behind it into one fma in spite of their .rn; it cannot join an fma whose
+// addend, -0, it does not know: a parameter of the kernel.)
+__device__ __forceinline__ f2 product(f2 a, f2 b, f2 minus_zero) { return f2_fma(a, b, minus_zero); }
+
 constexpr int kThreads = 256;
 constexpr int kEach = 8;                           // consecutive elements of a thread
-constexpr int kRounds = 2;                         // groups of them it takes in turn
-constexpr int kChunk = kThreads * kEach * kRounds;  // elements of a block
+constexpr int kPairs = kEach / 2;
+constexpr int kChunk = kThreads * kEach;           // elements of a block: one group a thread
 
 __device__ __forceinline__ uint32_t stir(uint32_t x) {
   x ^= x >> 16;
@@ -70,8 +79,12 @@ __device__ __forceinline__ Hyper hyper_of(const AdamWStep& a) {
   return h;
 }
 
-__device__ __forceinline__ uint32_t random_bits(uint32_t k1, uint32_t k2, int64_t i) {
-  uint32_t x = static_cast<uint32_t>(i) + static_cast<uint32_t>(i >> 32) * 0x3C6EF373u + k1;
+// The 32 random bits of element i: random_bits(first_word(k1, i), k2), and of the j-th
+// after it, with no carry in between (i a multiple of 8, j < 8), + j.
+__device__ __forceinline__ uint32_t first_word(uint32_t k1, int64_t i) {
+  return static_cast<uint32_t>(i) + static_cast<uint32_t>(i >> 32) * 0x3C6EF373u + k1;
+}
+__device__ __forceinline__ uint32_t random_bits(uint32_t x, uint32_t k2) {
   x ^= x >> 16;
   x = (x * 0x9E3779B1u) ^ k2;
   x ^= x >> 15;
@@ -90,39 +103,52 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
   return b > 0 ? static_cast<uint32_t>(b) : 0u;
 }
 
-// |v| / 2^k as an e4m3 code, inv = 2^-k: the product with 2^-120 puts e4m3's
-// exponents on fp32's lowest ones, subnormal numbers included, so the code is the
-// word's top bits; `low` is the 16-bit random number times 16.
-__device__ __forceinline__ uint32_t e4m3_code(float mag, float inv, uint32_t low) {
-  return (__float_as_uint(__fmul_rn(__fmul_rn(mag, inv), 0x1p-120f)) + low + 8u) >> 20;
+// |v| / 2^k of a pair, inv = 2^-k, times 2^-120: that puts e4m3's exponents on
+// fp32's lowest ones, subnormal numbers included, so that an e4m3 code is the bits
+// 20 .. 26 of the word.
+__device__ __forceinline__ f2 scaled_pair(f2 mag, f2 inv) {
+  return f2_mul(f2_mul(mag, inv), f2_set(0x1p-120f));
+}
+// The stochastically rounded code of such a word in the top byte: the 20 bits below the
+// code get the random 16-bit number (half HIGH of rnd) and a half of its last place,
+// and the word moves up by 4 bits.
+template <bool HIGH>
+__device__ __forceinline__ uint32_t code_on_top(float y, uint32_t rnd) {
+  const uint32_t add = __byte_perm(rnd, 0x00000080u, HIGH ? 0x5324 : 0x5104);
+  return __float_as_uint(y) * 16u + add;
+}
+// The top bytes of four words.
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
 }
 
 // kEach elements from i on, `count` of them in the tensor (zeros behind it): in
 // 16-byte accesses (8 for codes) where WHOLE, else one by one.
 template <bool WHOLE>
-__device__ __forceinline__ void load(float (&v)[kEach], const float* p, int count) {
+__device__ __forceinline__ void load(f2 (&v)[kPairs], const float* p, int count) {
   if constexpr (WHOLE) {
     const float4 lo = reinterpret_cast<const float4*>(p)[0], hi = reinterpret_cast<const float4*>(p)[1];
-    v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w;
-    v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
+    v[0] = f2_pack(lo.x, lo.y), v[1] = f2_pack(lo.z, lo.w);
+    v[2] = f2_pack(hi.x, hi.y), v[3] = f2_pack(hi.z, hi.w);
   } else {
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) v[j] = j < count ? p[j] : 0.0f;
+    for (int j = 0; j < kPairs; ++j)
+      v[j] = f2_pack(2 * j < count ? p[2 * j] : 0.0f, 2 * j + 1 < count ? p[2 * j + 1] : 0.0f);
   }
 }
 template <bool WHOLE>
-__device__ __forceinline__ void load(float (&v)[kEach], const __nv_bfloat16* p, int count) {
+__device__ __forceinline__ void load(f2 (&v)[kPairs], const __nv_bfloat16* p, int count) {
   if constexpr (WHOLE) {
     const uint4 q = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    const uint32_t w[kPairs] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(w[j] << 16);
-      v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-    }
+    for (int j = 0; j < kPairs; ++j)
+      v[j] = f2_pack(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
   } else {
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) v[j] = j < count ? __bfloat162float(p[j]) : 0.0f;
+    for (int j = 0; j < kPairs; ++j)
+      v[j] = f2_pack(2 * j < count ? __bfloat162float(p[2 * j]) : 0.0f,
+                     2 * j + 1 < count ? __bfloat162float(p[2 * j + 1]) : 0.0f);
   }
 }
 template <bool WHOLE>
@@ -135,30 +161,35 @@ __device__ __forceinline__ uint2 load_codes(const uint8_t* p, int count) {
   return make_uint2(w[0], w[1]);
 }
 template <bool WHOLE>
-__device__ __forceinline__ void store(float* p, const float (&v)[kEach], int count) {
+__device__ __forceinline__ void store(float* p, const f2 (&v)[kPairs], int count) {
+  float e[kEach];
+#pragma unroll
+  for (int j = 0; j < kPairs; ++j) f2_unpack(v[j], e[2 * j], e[2 * j + 1]);
   if constexpr (WHOLE) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    reinterpret_cast<float4*>(p)[0] = make_float4(e[0], e[1], e[2], e[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(e[4], e[5], e[6], e[7]);
   } else {
 #pragma unroll
     for (int j = 0; j < kEach; ++j)
-      if (j < count) p[j] = v[j];
+      if (j < count) p[j] = e[j];
   }
 }
 template <bool WHOLE>
-__device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[kEach], int count) {
-  if constexpr (WHOLE) {
-    uint32_t w[4];
+__device__ __forceinline__ void store(__nv_bfloat16* p, const f2 (&v)[kPairs], int count) {
+  uint32_t w[kPairs];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-      w[j] = *reinterpret_cast<const uint32_t*>(&h);
-    }
+  for (int j = 0; j < kPairs; ++j) {
+    float lo, hi;
+    f2_unpack(v[j], lo, hi);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    w[j] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  if constexpr (WHOLE) {
     *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
 #pragma unroll
     for (int j = 0; j < kEach; ++j)
-      if (j < count) p[j] = __float2bfloat16_rn(v[j]);
+      if (j < count) p[j] = __ushort_as_bfloat16(static_cast<uint16_t>(w[j / 2] >> (j % 2 * 16)));
   }
 }
 template <bool WHOLE>
@@ -173,22 +204,27 @@ __device__ __forceinline__ void store_codes(uint8_t* p, uint2 w, int count) {
 }
 
 // Eight e4m3 codes times their scale.
-__device__ __forceinline__ void decode(float (&v)[kEach], uint2 codes, float scale) {
+__device__ __forceinline__ void decode(f2 (&v)[kPairs], uint2 codes, float scale) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < kPairs; ++j) {
     const uint32_t two = (j < 2 ? codes.x : codes.y) >> (j % 2 * 16) & 0xFFFFu;
     const __half2_raw h =
         __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
     const float2 f = __half22float2(__half2(h));
-    v[2 * j] = f.x * scale;
-    v[2 * j + 1] = f.y * scale;
+    v[j] = f2_mul(f2_pack(f.x, f.y), f2_set(scale));
   }
 }
 
-// The root for the division alone (32-bit moments): one instruction, off by an ulp.
+// For the division alone: one instruction each.  (Denominators lie far from the
+// numbers that .ftz drops: a positive root is at least 2^-75, a finite one below 2^65.)
 __device__ __forceinline__ float root_fast(float v) {
   float r;
   asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float rcp_fast(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
 
@@ -198,7 +234,7 @@ template <bool BITS8, bool WHOLE>
 __device__ __forceinline__ void step_elements(const AdamWStep& a, const Hyper& h,
                                               const AdamWTensor& t, uint32_t k2, int64_t i,
                                               int count) {
-  float p[kEach], g[kEach], m[kEach], v[kEach];
+  f2 p[kPairs], g[kPairs], m[kPairs], v[kPairs];
   uint2 cm = make_uint2(0u, 0u), cr = cm;
   uint32_t sm = 0u, sr = 0u;
   if (t.master)
@@ -221,19 +257,24 @@ __device__ __forceinline__ void step_elements(const AdamWStep& a, const Hyper& h
     decode(m, cm, e8m0_value(sm));
     decode(v, cr, e8m0_value(sr));
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) v[j] = __fmul_rn(v[j], v[j]);
+    for (int j = 0; j < kPairs; ++j) v[j] = f2_mul(v[j], v[j]);
   } else {
     load<WHOLE>(m, static_cast<const float*>(t.exp_avg) + i, count);
     load<WHOLE>(v, static_cast<const float*>(t.exp_avg_sq) + i, count);
   }
+  const f2 nz = f2_set(a.minus_zero);
+  f2 root[kPairs];
 #pragma unroll
-  for (int j = 0; j < kEach; ++j) {
-    m[j] = __fadd_rn(__fmul_rn(m[j], a.beta1), __fmul_rn(g[j], a.one_beta1));
-    v[j] = __fadd_rn(__fmul_rn(v[j], a.beta2), __fmul_rn(__fmul_rn(g[j], g[j]), a.one_beta2));
-    const float r = BITS8 ? __fsqrt_rn(v[j]) : root_fast(v[j]);
-    const float denom = __fmaf_rn(r, h.inv_sqrt_bc2, a.eps);
-    p[j] = __fmaf_rn(-h.step_size, __fdividef(m[j], denom), p[j] * h.decay);
-    if (BITS8) v[j] = r;
+  for (int j = 0; j < kPairs; ++j) {
+    m[j] = f2_add(product(m[j], f2_set(a.beta1), nz), product(g[j], f2_set(a.one_beta1), nz));
+    v[j] = f2_add(product(v[j], f2_set(a.beta2), nz),
+                  product(product(g[j], g[j], nz), f2_set(a.one_beta2), nz));
+    float lo, hi;
+    f2_unpack(v[j], lo, hi);
+    root[j] = BITS8 ? f2_pack(__fsqrt_rn(lo), __fsqrt_rn(hi)) : f2_pack(root_fast(lo), root_fast(hi));
+    f2_unpack(f2_fma(root[j], f2_set(h.inv_sqrt_bc2), f2_set(a.eps)), lo, hi);
+    const f2 step = f2_mul(m[j], f2_pack(rcp_fast(lo), rcp_fast(hi)));
+    p[j] = f2_fma(step, f2_set(-h.step_size), f2_mul(p[j], f2_set(h.decay)));
   }
   if (t.master) store<WHOLE>(t.master + i, p, count);
   if (a.param_bf16)
@@ -243,9 +284,12 @@ __device__ __forceinline__ void step_elements(const AdamWStep& a, const Hyper& h
   if constexpr (BITS8) {
     uint32_t tm = 0u, tr = 0u;  // the largest magnitudes' bits
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-      tm = max(tm, __float_as_uint(m[j]) & 0x7FFFFFFFu);
-      tr = max(tr, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    for (int j = 0; j < kPairs; ++j) {
+      float lo, hi;
+      f2_unpack(m[j], lo, hi);
+      tm = max(tm, max(__float_as_uint(lo) & 0x7FFFFFFFu, __float_as_uint(hi) & 0x7FFFFFFFu));
+      f2_unpack(root[j], lo, hi);
+      tr = max(tr, max(__float_as_uint(lo), __float_as_uint(hi)));
     }
 #pragma unroll
     for (int o = 1; o < 32 / kEach; o *= 2) {
@@ -254,22 +298,30 @@ __device__ __forceinline__ void step_elements(const AdamWStep& a, const Hyper& h
     }
     sm = scale_byte(tm);
     sr = scale_byte(tr);
-    // a block with a NaN scale keeps any codes: zeros
-    const float im = sm == 255u ? 0.0f : __uint_as_float((254u - sm) << 23);
-    const float ir = sr == 255u ? 0.0f : __uint_as_float((254u - sr) << 23);
-    uint32_t wm[2] = {0u, 0u}, wr[2] = {0u, 0u};
+    // (a block with the scale 255 is NaN whatever its codes are)
+    const f2 im = f2_set(__uint_as_float((254u - min(sm, 254u)) << 23));
+    const f2 ir = f2_set(__uint_as_float((254u - min(sr, 254u)) << 23));
+    const uint32_t word = first_word(h.key, i);
+    uint32_t wm[kEach], wr[kEach];
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-      const uint32_t rnd = random_bits(h.key, k2, i + j);
-      const float mag = sm == 255u ? 0.0f : fabsf(m[j]), root = sr == 255u ? 0.0f : v[j];
-      const uint32_t sign = __float_as_uint(m[j]) >> 31 << 7;
-      const uint32_t code_m = e4m3_code(mag, im, (rnd & 0xFFFFu) << 4) | sign;
-      const uint32_t code_r = max(e4m3_code(root, ir, rnd >> 16 << 4), root > 0.0f ? 1u : 0u);
-      wm[j / 4] |= code_m << (j % 4 * 8);
-      wr[j / 4] |= code_r << (j % 4 * 8);
+    for (int j = 0; j < kPairs; ++j) {
+      const uint32_t rnd0 = random_bits(word + 2 * j, k2);
+      const uint32_t rnd1 = random_bits(word + 2 * j + 1, k2);
+      float lo, hi, y0, y1;
+      f2_unpack(m[j], lo, hi);
+      f2_unpack(scaled_pair(m[j] & 0x7FFFFFFF7FFFFFFFull, im), y0, y1);
+      wm[2 * j] = code_on_top<false>(y0, rnd0) | (__float_as_uint(lo) & 0x80000000u);
+      wm[2 * j + 1] = code_on_top<false>(y1, rnd1) | (__float_as_uint(hi) & 0x80000000u);
+      f2_unpack(root[j], lo, hi);
+      f2_unpack(scaled_pair(root[j], ir), y0, y1);
+      // at least code 1 for a positive root (whose bits are above 0x01000000)
+      wr[2 * j] = max(code_on_top<true>(y0, rnd0), min(__float_as_uint(lo), 0x01000000u));
+      wr[2 * j + 1] = max(code_on_top<true>(y1, rnd1), min(__float_as_uint(hi), 0x01000000u));
     }
-    store_codes<WHOLE>(static_cast<uint8_t*>(t.exp_avg) + i, make_uint2(wm[0], wm[1]), count);
-    store_codes<WHOLE>(static_cast<uint8_t*>(t.exp_avg_sq) + i, make_uint2(wr[0], wr[1]), count);
+    cm = make_uint2(top_bytes(wm[0], wm[1], wm[2], wm[3]), top_bytes(wm[4], wm[5], wm[6], wm[7]));
+    cr = make_uint2(top_bytes(wr[0], wr[1], wr[2], wr[3]), top_bytes(wr[4], wr[5], wr[6], wr[7]));
+    store_codes<WHOLE>(static_cast<uint8_t*>(t.exp_avg) + i, cm, count);
+    store_codes<WHOLE>(static_cast<uint8_t*>(t.exp_avg_sq) + i, cr, count);
     if (threadIdx.x % (32 / kEach) == 0 && count > 0) {
       t.exp_avg_scale[i / 32] = static_cast<uint8_t>(sm);
       t.exp_avg_sq_scale[i / 32] = static_cast<uint8_t>(sr);
@@ -281,7 +333,7 @@ __device__ __forceinline__ void step_elements(const AdamWStep& a, const Hyper& h
 }
 
 template <bool BITS8, int CAP>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, BITS8 ? 6 : 5)
     adamw_kernel(const __grid_constant__ AdamWStep a, const __grid_constant__ AdamWList<CAP> l) {
   pdl_wait();
   const Hyper h = hyper_of(a);
@@ -297,18 +349,15 @@ __global__ void __launch_bounds__(kThreads)
   const AdamWTensor t = l.tensors[lo];
   const uint32_t k2 = stir(h.key + 0xBB67AE85u * static_cast<uint32_t>(l.first_tensor + lo + 1));
   const int64_t base = static_cast<int64_t>(blockIdx.x - l.first_block[lo]) * kChunk;
-#pragma unroll 1
-  for (int k = 0; k < kRounds; ++k) {
-    // the warp's first element: its threads go one way
-    const int64_t w = base + (k * kThreads + threadIdx.x / 32 * 32) * kEach;
-    if (w >= t.n) break;
-    const int64_t i = w + threadIdx.x % 32 * kEach;
-    if (t.whole && w + 32 * kEach <= t.n)
-      step_elements<BITS8, true>(a, h, t, k2, i, kEach);
-    else
-      step_elements<BITS8, false>(a, h, t, k2, i,
-                                  static_cast<int>(max(int64_t(0), min(t.n - i, int64_t(kEach)))));
-  }
+  // the warp's first element: its threads go one way
+  const int64_t w = base + threadIdx.x / 32 * 32 * kEach;
+  if (w >= t.n) return;
+  const int64_t i = w + threadIdx.x % 32 * kEach;
+  if (t.whole && w + 32 * kEach <= t.n)
+    step_elements<BITS8, true>(a, h, t, k2, i, kEach);
+  else
+    step_elements<BITS8, false>(a, h, t, k2, i,
+                                static_cast<int>(max(int64_t(0), min(t.n - i, int64_t(kEach)))));
 }
 
 }  // namespace

@@ -313,6 +313,7 @@ struct AdamWTensor {
 };
 struct AdamWStep {
   float beta1, one_beta1, beta2, one_beta2, eps;
+  float minus_zero;                            // -0.0f (see product() in adamw.cu)
   float step_size, inv_sqrt_bc2, decay;        // of the host's step number and rate
   double lr, weight_decay, log_beta1, log_beta2;  // for the device's
   int64_t step;

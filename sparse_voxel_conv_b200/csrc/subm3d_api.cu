@@ -774,6 +774,7 @@ subm3d_status subm3d_adamw(const subm3d_adamw_tensor* tensors, int32_t count,
   a.beta2 = static_cast<float>(c.beta2);
   a.one_beta2 = static_cast<float>(1.0 - c.beta2);
   a.eps = static_cast<float>(c.eps);
+  a.minus_zero = -0.0f;
   a.lr = c.lr;
   a.weight_decay = c.weight_decay;
   a.log_beta1 = std::log(c.beta1);
