@@ -8,6 +8,7 @@ there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -106,8 +107,8 @@ lib = _load()
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # torch's current stream on the current device
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -288,11 +289,12 @@ def subm3d_layer_norm(x, n: int, channels: int, x_stride: int, dtype: int, weigh
     st = lib.subm3d_layer_norm(_ptr(x), n, channels, x_stride, dtype, _ptr(weight), _ptr(bias),
                                affine_dtype, eps, act, _ptr(y), _ptr(mean), _ptr(rstd),
                                _stream(stream))
-    _check(st, "subm3d_layer_norm")
+    if st:
+        _check(st, "subm3d_layer_norm")
 
 
 def subm3d_layer_norm_workspace_bytes(n: int, channels: int) -> int:
-    return int(lib.subm3d_layer_norm_workspace_bytes(int(n), int(channels)))
+    return lib.subm3d_layer_norm_workspace_bytes(n, channels)
 
 
 def subm3d_layer_norm_backward(dy, dy_stride: int, x, x_stride: int, n: int, channels: int,
@@ -307,11 +309,16 @@ def subm3d_layer_norm_backward(dy, dy_stride: int, x, x_stride: int, n: int, cha
     _check(st, "subm3d_layer_norm_backward")
 
 
+@functools.lru_cache(maxsize=64)
+def _int32_array(values):
+    return (ctypes.c_int32 * len(values))(*values)
+
+
 def subm3d_rotary(x, x_row: int, x_head: int, n: int, heads: int, head_dim: int, dtype: int,
                   positions, positions_f32: bool, pos_stride: int, axis_pairs, theta: float,
                   halves: bool, inverse: bool, y, y_row: int, y_head: int, stream=None) -> None:
     """Enqueue y = x turned by its rows' positions (axis_pairs: pairs per axis)."""
-    pairs = (ctypes.c_int32 * len(axis_pairs))(*axis_pairs)
+    pairs = _int32_array(tuple(axis_pairs))
     st = lib.subm3d_rotary(_ptr(x), x_row, x_head, n, heads, head_dim, dtype, _ptr(positions),
                            1 if positions_f32 else 0, pos_stride, len(axis_pairs), pairs, theta,
                            1 if halves else 0, 1 if inverse else 0, _ptr(y), y_row, y_head,
@@ -327,6 +334,12 @@ class AdamWTensor(ctypes.Structure):
                 ("master", ctypes.c_void_p), ("n", ctypes.c_int64)]
 
 
+def adamw_tensors(rows):
+    """subm3d_adamw_tensor[] from one 8-tuple a tensor, in the fields' order (eight
+    64-bit words each)."""
+    return (ctypes.c_int64 * (8 * len(rows)))(*[v for row in rows for v in row])
+
+
 class AdamWStep(ctypes.Structure):
     """subm3d_adamw_step: one step's numbers."""
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
@@ -338,7 +351,7 @@ class AdamWStep(ctypes.Structure):
 
 
 def subm3d_adamw(tensors, count: int, step: AdamWStep, stream=None) -> None:
-    """Enqueue one step over `count` tensors (an array of AdamWTensor)."""
+    """Enqueue one step over `count` tensors (an array of subm3d_adamw_tensor)."""
     st = lib.subm3d_adamw(tensors, int(count), ctypes.byref(step), _stream(stream))
     _check(st, "subm3d_adamw")
 

@@ -2,8 +2,6 @@
 tensor argument, and the rules for calls on another stream or device."""
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from . import _abi
@@ -49,24 +47,26 @@ def _on_side_stream(stream, *made) -> None:
             t.record_stream(side)
 
 
-def _same_device(dev: torch.device, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+def _device_of(t: torch.Tensor, name: str) -> int:
+    """The CUDA device's index of a tensor argument."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
 
 
-_HERE = contextlib.nullcontext()
+def _same_device(dev: int, name: str, t) -> None:
+    if t is not None and t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
 
 
-def _on_device(dev: torch.device):
-    """A context in which `dev` is the current device (the library works on the
-    current one, and so does torch's current stream)."""
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        return _HERE
-    return torch.cuda.device(dev)
+# The current device's index (what torch.cuda.current_device() returns once CUDA is up,
+# without its start-up checks): the library works on the current device, so a call on
+# tensors of another one is made again with that device current.
+_current_device = torch._C._cuda_getDevice
 
 
-def _written(*tensors) -> None:
+def _written(tensors) -> None:
     """Tells autograd that the library wrote these tensors in place, so that a
     backward pass that had saved one of them fails instead of using the new values."""
-    torch.autograd.graph.increment_version([t for t in tensors if t is not None])
+    torch.autograd.graph.increment_version(tensors)

@@ -626,11 +626,12 @@ subm3d_status subm3d_rotary(const void* x, int64_t x_row, int64_t x_head, int64_
   if (head_dim % 2 != 0 || head_dim / 2 > subm3d::kRotaryMaxPairs) return SUBM3D_E_UNSUPPORTED;
   subm3d::RotaryArgs a;
   int64_t used = 0;
+  const double log_theta = std::log(theta);
   for (int i = 0; i < axes; ++i) {
     if (axis_pairs[i] < 0 || axis_pairs[i] > head_dim / 2 - used) return SUBM3D_E_INVALID;
     a.axis_pairs[i] = axis_pairs[i];
     for (int j = 0; j < axis_pairs[i]; ++j)
-      a.turns[used + j] = std::exp(-std::log(theta) * j / axis_pairs[i]) / 6.283185307179586476925;
+      a.turns[used + j] = std::exp(-log_theta * j / axis_pairs[i]) / 6.283185307179586476925;
     used += axis_pairs[i];
   }
   if (n == 0 || heads == 0) return SUBM3D_OK;

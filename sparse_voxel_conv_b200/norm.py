@@ -11,74 +11,80 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _abi
-from ._host import _ACTS, _DTYPES, _new, _on_device, _on_side_stream, _same_device, _written
+from ._host import _ACTS, _DTYPES, _current_device, _device_of, _new, _on_side_stream, \
+    _same_device, _written
 
 __all__ = ["layer_norm", "layer_norm_forward", "layer_norm_backward", "LayerNorm"]
 
 
-def _rows(t: torch.Tensor, name: str, dtype=None):
+def _rows(t: torch.Tensor, name: str):
     """t as rows of its last dimension: (tensor, row stride), a view where it can be."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() == 0 or t.shape[-1] == 0:
+    shape = t.shape
+    if not shape or shape[-1] == 0:
         raise ValueError(f"{name} must have at least one channel")
-    c = t.shape[-1]
-    if t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= c:
-        return t, t.stride(0)
+    c = shape[-1]
+    if len(shape) == 2:
+        row, col = t.stride()
+        if col == 1 and row >= c:
+            return t, row
     return t.contiguous(), c
 
 
-def _affine(t, name: str, x: torch.Tensor):
-    if t is None:
-        return None
-    if t.dtype != torch.float32 and t.dtype != x.dtype:
-        raise ValueError(f"{name} must be float32 or {x.dtype}, got {t.dtype}")
-    if t.dim() != 1 or t.shape[0] != x.shape[-1]:
-        raise ValueError(f"{name} must have shape [{x.shape[-1]}]")
+def _affine(t, name: str, x_dtype, c: int, dev: int):
+    if t.dtype is not torch.float32 and t.dtype is not x_dtype:
+        raise ValueError(f"{name} must be float32 or {x_dtype}, got {t.dtype}")
+    if t.shape != (c,):
+        raise ValueError(f"{name} must have shape [{c}]")
+    _same_device(dev, name, t)
     return t.contiguous()
 
 
-def _affine_code(weight, bias, x: torch.Tensor) -> int:
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
-        raise ValueError("weight and bias must have one dtype")
-    first = weight if weight is not None else bias
-    return _DTYPES[x.dtype if first is None else first.dtype]
+def _affine_of(weight, bias, x_dtype, c: int, dev: int):
+    """(weight, bias, type code) checked."""
+    if weight is not None:
+        weight = _affine(weight, "weight", x_dtype, c, dev)
+    if bias is not None:
+        bias = _affine(bias, "bias", x_dtype, c, dev)
+        if weight is not None and weight.dtype is not bias.dtype:
+            raise ValueError("weight and bias must have one dtype")
+        return weight, bias, _DTYPES[bias.dtype]
+    return weight, bias, _DTYPES[x_dtype if weight is None else weight.dtype]
 
 
-def _codes(x: torch.Tensor, act):
-    if x.dtype not in _DTYPES:
-        raise ValueError(f"unsupported dtype {x.dtype}")
+def _codes(dtype, act):
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
     if act not in _ACTS:
         raise ValueError(f"unknown activation {act!r}")
-    return _DTYPES[x.dtype], _ACTS[act]
+    return _DTYPES[dtype], _ACTS[act]
 
 
 def _norm(x, weight, bias, eps, act, out, stream, stats: bool):
-    dtype, act_code = _codes(x, act)
+    dev = _device_of(x, "x")
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return _norm(x, weight, bias, eps, act, out, stream, stats)
+    x_dtype = x.dtype
+    dtype, act_code = _codes(x_dtype, act)
     rows, stride = _rows(x, "x")
-    w, b = _affine(weight, "weight", x), _affine(bias, "bias", x)
-    affine_dtype = _affine_code(w, b, x)
-    dev = x.device
-    _same_device(dev, weight=w, bias=b, out=out)
     c = x.shape[-1]
     n = x.numel() // c
-    with _on_device(dev):
-        if out is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        else:
-            if out.shape != x.shape or out.dtype != x.dtype or not out.is_contiguous():
-                raise ValueError(f"out must be a contiguous {x.dtype} tensor of x's shape")
-            y = out
-        mean = rstd = None
-        if stats:
-            mean, rstd = torch.empty((2, n), dtype=torch.float32, device=dev).unbind()
-        if stream is not None:
-            _on_side_stream(stream, _new(rows, x), _new(w, weight), _new(b, bias), _new(y, out),
-                            mean, rstd)
-        _abi.subm3d_layer_norm(rows, n, c, stride, dtype, w, b, affine_dtype, eps, act_code, y,
-                               mean, rstd, stream)
+    w, b, affine_dtype = _affine_of(weight, bias, x_dtype, c, dev)
+    if out is None:
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    else:
+        _same_device(dev, "out", out)
+        if out.shape != x.shape or out.dtype != x_dtype or not out.is_contiguous():
+            raise ValueError(f"out must be a contiguous {x_dtype} tensor of x's shape")
+        y = out
+    mean = rstd = None
+    if stats:
+        mean, rstd = y.new_empty((2, n), dtype=torch.float32).unbind()
+    if stream is not None:
+        _on_side_stream(stream, _new(rows, x), _new(w, weight), _new(b, bias), _new(y, out),
+                        mean, rstd)
+    _abi.subm3d_layer_norm(rows, n, c, stride, dtype, w, b, affine_dtype, eps, act_code, y, mean,
+                           rstd, stream)
     if out is not None:
         _written(out)
     return y, mean, rstd
@@ -104,35 +110,41 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
     which of the three to compute; the others are None, and so are dweight without
     a weight and dbias without a bias.
     """
-    dtype, act_code = _codes(x, act)
-    if dy.shape != x.shape:
-        raise ValueError("dy must have x's shape")
+    dev = _device_of(x, "x")
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return layer_norm_backward(dy, x, mean, rstd, weight, bias, act, wanted, stream)
+    x_dtype = x.dtype
+    dtype, act_code = _codes(x_dtype, act)
+    if dy.shape != x.shape or dy.dtype != x_dtype:
+        raise ValueError("dy must have x's shape and dtype")
     xr, x_stride = _rows(x, "x")
-    dr, dy_stride = _rows(dy, "dy", x.dtype)
-    w, b = _affine(weight, "weight", x), _affine(bias, "bias", x)
-    affine_dtype = _affine_code(w, b, x)
-    dev = x.device
+    dr, dy_stride = _rows(dy, "dy")
     c = x.shape[-1]
     n = x.numel() // c
+    w, b, affine_dtype = _affine_of(weight, bias, x_dtype, c, dev)
+    _same_device(dev, "dy", dy)
     for name, t in (("mean", mean), ("rstd", rstd)):
-        if t.dtype != torch.float32 or t.numel() != n:
+        if t.dtype is not torch.float32 or t.numel() != n:
             raise ValueError(f"{name} must be float32 with one value a row ({n})")
+        _same_device(dev, name, t)
     mean_c, rstd_c = mean.contiguous(), rstd.contiguous()
-    _same_device(dev, dy=dr, mean=mean_c, rstd=rstd_c, weight=w, bias=b)
-    with _on_device(dev):
-        dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if wanted[0] else None
-        dw = torch.empty(c, dtype=torch.float32, device=dev) if wanted[1] and w is not None else None
-        db = torch.empty(c, dtype=torch.float32, device=dev) if wanted[2] and b is not None else None
-        ws, ws_bytes = None, 0
-        if dw is not None or db is not None:
-            ws_bytes = _abi.subm3d_layer_norm_workspace_bytes(n, c)
-            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-        if stream is not None:
-            _on_side_stream(stream, dx, dw, db, ws, _new(xr, x), _new(dr, dy), _new(w, weight),
-                            _new(b, bias), _new(mean_c, mean), _new(rstd_c, rstd))
-        _abi.subm3d_layer_norm_backward(dr, dy_stride, xr, x_stride, n, c, dtype, mean_c, rstd_c,
-                                        w, b, affine_dtype, act_code, dx, dw, db, ws, ws_bytes,
-                                        stream)
+    want_dx, want_dw, want_db = wanted
+    dx = torch.empty_like(x, memory_format=torch.contiguous_format) if want_dx else None
+    dw = db = ws = None
+    ws_bytes = 0
+    if want_dw and w is not None:
+        dw = mean_c.new_empty(c)
+    if want_db and b is not None:
+        db = mean_c.new_empty(c)
+    if dw is not None or db is not None:
+        ws_bytes = _abi.subm3d_layer_norm_workspace_bytes(n, c)
+        ws = mean_c.new_empty(ws_bytes // 4)
+    if stream is not None:
+        _on_side_stream(stream, dx, dw, db, ws, _new(xr, x), _new(dr, dy), _new(w, weight),
+                        _new(b, bias), _new(mean_c, mean), _new(rstd_c, rstd))
+    _abi.subm3d_layer_norm_backward(dr, dy_stride, xr, x_stride, n, c, dtype, mean_c, rstd_c, w,
+                                    b, affine_dtype, act_code, dx, dw, db, ws, ws_bytes, stream)
     return dx, dw, db
 
 

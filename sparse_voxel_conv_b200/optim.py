@@ -8,7 +8,7 @@ from __future__ import annotations
 import torch
 
 from . import _abi
-from ._host import _DTYPES, _on_device, _on_side_stream, _written
+from ._host import _DTYPES, _current_device, _device_of, _on_side_stream, _written
 
 __all__ = ["adamw_step", "AdamW"]
 
@@ -16,26 +16,26 @@ _BLOCK = 32  # elements that share a scale of the 8-bit moments
 _CODE, _SCALE = torch.float8_e4m3fn, torch.float8_e8m0fnu
 
 
-def _each(name, tensors, like, dtype, sizes=None):
-    """Checks a list that runs along the parameters: their number, type, device,
-    sizes and layout."""
-    if len(tensors) != len(like):
-        raise ValueError(f"{name} must have one tensor for each of {len(like)} parameters")
-    dev = like[0].device
-    for i, (t, p) in enumerate(zip(tensors, like)):
-        if t.dtype != dtype:
+def _each(name, tensors, dtype, dev: int, sizes):
+    """The addresses of a list that runs along the parameters, after a check of their
+    number, type, device, sizes and layout."""
+    if len(tensors) != len(sizes):
+        raise ValueError(f"{name} must have one tensor for each of {len(sizes)} parameters")
+    for i, (t, n) in enumerate(zip(tensors, sizes)):
+        if t.dtype is not dtype:
             raise ValueError(f"{name}[{i}] must be {dtype}, got {t.dtype}")
-        if t.device != dev:
-            raise ValueError(f"{name}[{i}] must be on {dev}, got {t.device}")
-        if t.numel() != (p.numel() if sizes is None else sizes[i]):
+        if t.get_device() != dev:
+            raise ValueError(f"{name}[{i}] must be on cuda:{dev}, got {t.device}")
+        if t.numel() != n:
             raise ValueError(f"{name}[{i}] has the wrong number of elements")
         if not t.is_contiguous():
             raise ValueError(f"{name}[{i}] must be contiguous")
+    return [t.data_ptr() for t in tensors]
 
 
-def _scalar(t, name, dtype, dev):
-    if t.numel() != 1 or t.dtype != dtype or t.device != dev:
-        raise ValueError(f"{name} as a tensor must be one {dtype} on {dev}")
+def _scalar(t, name, dtype, dev: int):
+    if t.numel() != 1 or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name} as a tensor must be one {dtype} on cuda:{dev}")
     return t.data_ptr()
 
 
@@ -60,57 +60,54 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0.9, 
     captured graph).  All tensors contiguous and on one device.  A tensor that is
     written may not share memory with another one.
     """
-    if len(params) == 0:
+    count = len(params)
+    if count == 0:
         return
-    dev = params[0].device
-    if not params[0].is_cuda:
-        raise ValueError("params must be CUDA tensors")
-    if len(grads) != len(params):
-        raise ValueError(f"grads must have one tensor for each of {len(params)} parameters")
-    p_type, g_type, s_type = params[0].dtype, grads[0].dtype, None
+    dev = _device_of(params[0], "params")
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas, eps,
+                              weight_decay, masters, exp_avg_scales, exp_avg_sq_scales, seed,
+                              stream)
+    if not len(grads) == len(exp_avgs) == count:
+        raise ValueError(f"grads and exp_avgs must have one tensor for each of {count} parameters")
+    p_type, g_type, s_type = params[0].dtype, grads[0].dtype, exp_avgs[0].dtype
     if p_type not in _DTYPES or g_type not in _DTYPES:
         raise ValueError(f"unsupported dtype {p_type} or {g_type}")
-    if len(exp_avgs) != len(params):
-        raise ValueError(f"exp_avgs must have one tensor for each of {len(params)} parameters")
-    s_type = exp_avgs[0].dtype
-    if s_type not in (torch.float32, _CODE):
+    bits8 = s_type is _CODE
+    if not bits8 and s_type is not torch.float32:
         raise ValueError(f"moments must be float32 or {_CODE}, got {s_type}")
-    bits8 = s_type == _CODE
-    _each("params", params, params, p_type)
-    _each("grads", grads, params, g_type)
-    _each("exp_avgs", exp_avgs, params, s_type)
-    _each("exp_avg_sqs", exp_avg_sqs, params, s_type)
-    if masters is not None:
-        _each("masters", masters, params, torch.float32)
+    sizes = [p.numel() for p in params]
+    none = (0,) * count
+    p_at = _each("params", params, p_type, dev, sizes)
+    g_at = _each("grads", grads, g_type, dev, sizes)
+    m_at = _each("exp_avgs", exp_avgs, s_type, dev, sizes)
+    v_at = _each("exp_avg_sqs", exp_avg_sqs, s_type, dev, sizes)
+    w_at = none if masters is None else _each("masters", masters, torch.float32, dev, sizes)
+    ms_at = vs_at = none
     if bits8:
         if exp_avg_scales is None or exp_avg_sq_scales is None:
             raise ValueError("8-bit moments need exp_avg_scales and exp_avg_sq_scales")
-        blocks = [(p.numel() + _BLOCK - 1) // _BLOCK for p in params]
-        _each("exp_avg_scales", exp_avg_scales, params, _SCALE, blocks)
-        _each("exp_avg_sq_scales", exp_avg_sq_scales, params, _SCALE, blocks)
+        blocks = [(n + _BLOCK - 1) // _BLOCK for n in sizes]
+        ms_at = _each("exp_avg_scales", exp_avg_scales, _SCALE, dev, blocks)
+        vs_at = _each("exp_avg_sq_scales", exp_avg_sq_scales, _SCALE, dev, blocks)
     elif exp_avg_scales is not None or exp_avg_sq_scales is not None:
         raise ValueError("32-bit moments have no scales")
-    c = _abi.AdamWStep(beta1=betas[0], beta2=betas[1], eps=eps, weight_decay=weight_decay,
-                       param_dtype=_DTYPES[p_type], grad_dtype=_DTYPES[g_type],
-                       state_bits=8 if bits8 else 32, seed=seed & 0xFFFFFFFF)
+    step_at = lr_at = None
     if isinstance(step, torch.Tensor):
-        c.step_device = _scalar(step, "step", torch.int32, dev)
-    else:
-        c.step = step
+        step, step_at = 0, _scalar(step, "step", torch.int32, dev)
     if isinstance(lr, torch.Tensor):
-        c.lr_device = _scalar(lr, "lr", torch.float32, dev)
-    else:
-        c.lr = lr
-    count = len(params)
-    at = lambda ts: (None,) * count if ts is None else [t.data_ptr() for t in ts]  # noqa: E731
-    array = (_abi.AdamWTensor * count)(*zip(at(params), at(grads), at(exp_avgs), at(exp_avg_sqs),
-                                            at(exp_avg_scales), at(exp_avg_sq_scales),
-                                            at(masters), [p.numel() for p in params]))
-    with _on_device(dev):
-        if stream is not None:
-            _on_side_stream(stream)
-        _abi.subm3d_adamw(array, count, c, stream)
-    _written(*params, *(masters or ()))
+        lr, lr_at = 0.0, _scalar(lr, "lr", torch.float32, dev)
+    if stream is not None:
+        _on_side_stream(stream)
+    _abi.subm3d_adamw(
+        _abi.adamw_tensors(list(zip(p_at, g_at, m_at, v_at, ms_at, vs_at, w_at, sizes))), count,
+        _abi.AdamWStep(lr, betas[0], betas[1], eps, weight_decay, step, step_at, lr_at,
+                       _DTYPES[p_type], _DTYPES[g_type], 8 if bits8 else 32, seed & 0xFFFFFFFF),
+        stream)
+    _written(params)
+    if masters is not None:
+        _written(masters)
 
 
 class AdamW(torch.optim.Optimizer):

@@ -11,23 +11,30 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _abi
-from ._host import _DTYPES, _new, _on_device, _on_side_stream, _same_device, _written
+from ._host import _DTYPES, _current_device, _device_of, _new, _on_side_stream, _same_device, \
+    _written
 
 __all__ = ["rotary", "VoxelRotary"]
 
 
 def _turn(x, positions, theta, axis_pairs, interleaved, inverse, out, stream):
-    if x.dtype not in _DTYPES:
-        raise ValueError(f"unsupported dtype {x.dtype}")
-    if not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor")
-    if x.dim() not in (2, 3):
+    dev = _device_of(x, "x")
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return _turn(x, positions, theta, axis_pairs, interleaved, inverse, out, stream)
+    dtype, shape = x.dtype, x.shape
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    if len(shape) == 3:
+        n, heads, d = shape
+    elif len(shape) == 2:
+        (n, d), heads = shape, 1
+    else:
         raise ValueError("x must have shape [N, heads, head_dim] or [N, head_dim]")
-    n, d = x.shape[0], x.shape[-1]
-    heads = x.shape[1] if x.dim() == 3 else 1
     if d < 2 or d % 2:
         raise ValueError("head_dim must be even")
-    if positions.dtype not in (torch.int32, torch.float32):
+    pos_f32 = positions.dtype is torch.float32
+    if not pos_f32 and positions.dtype is not torch.int32:
         raise ValueError(f"positions must be int32 or float32, got {positions.dtype}")
     if positions.dim() != 2 or positions.shape[0] != n or not 1 <= positions.shape[1] <= 4:
         raise ValueError(f"positions must have shape [{n}, 1 to 4 axes]")
@@ -36,29 +43,28 @@ def _turn(x, positions, theta, axis_pairs, interleaved, inverse, out, stream):
         axis_pairs = (d // 2 // axes,) * axes
     elif len(axis_pairs) != axes or min(axis_pairs) < 0 or sum(axis_pairs) > d // 2:
         raise ValueError(f"axis_pairs must give each of {axes} axes its pairs, {d // 2} at most")
-    dev = x.device
-    _same_device(dev, positions=positions, out=out)
-    given = (x, positions)
+    _same_device(dev, "positions", positions)
+    x_in, pos_in = x, positions
     if x.stride(-1) != 1:
         if out is x:
             raise ValueError("x must have contiguous channels to be turned in place")
         x = x.contiguous()
     if positions.stride(1) != 1:
         positions = positions.contiguous()
-    with _on_device(dev):
-        if out is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        else:
-            if out.shape != x.shape or out.dtype != x.dtype or out.stride(-1) != 1:
-                raise ValueError(f"out must be {x.dtype} of x's shape with contiguous channels")
-            y = out
-        if stream is not None:
-            _on_side_stream(stream, _new(x, given[0]), _new(positions, given[1]), _new(y, out))
-        one = x.dim() == 2
-        _abi.subm3d_rotary(x, x.stride(0), 0 if one else x.stride(1), n, heads, d,
-                           _DTYPES[x.dtype], positions, positions.dtype == torch.float32,
-                           positions.stride(0), axis_pairs, theta, not interleaved, inverse, y,
-                           y.stride(0), d if one else y.stride(1), stream)
+    if out is None:
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    else:
+        _same_device(dev, "out", out)
+        if out.shape != shape or out.dtype != dtype or out.stride(-1) != 1:
+            raise ValueError(f"out must be {dtype} of x's shape with contiguous channels")
+        y = out
+    if stream is not None:
+        _on_side_stream(stream, _new(x, x_in), _new(positions, pos_in), _new(y, out))
+    xs, ys = x.stride(), y.stride()
+    x_head, y_head = (xs[1], ys[1]) if len(shape) == 3 else (0, d)
+    _abi.subm3d_rotary(x, xs[0], x_head, n, heads, d, _DTYPES[dtype], positions, pos_f32,
+                       positions.stride(0), axis_pairs, theta, not interleaved, inverse, y, ys[0],
+                       y_head, stream)
     if out is not None:
         _written(out)
     return y
