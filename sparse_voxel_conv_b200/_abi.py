@@ -7,9 +7,11 @@ there is no fallback.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 import os
+import struct
 
 import torch
 
@@ -334,12 +336,6 @@ class AdamWTensor(ctypes.Structure):
                 ("master", ctypes.c_void_p), ("n", ctypes.c_int64)]
 
 
-def adamw_tensors(rows):
-    """subm3d_adamw_tensor[] from one 8-tuple a tensor, in the fields' order (eight
-    64-bit words each)."""
-    return (ctypes.c_int64 * (8 * len(rows)))(*[v for row in rows for v in row])
-
-
 class AdamWStep(ctypes.Structure):
     """subm3d_adamw_step: one step's numbers."""
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
@@ -350,9 +346,22 @@ class AdamWStep(ctypes.Structure):
                 ("seed", ctypes.c_uint32)]
 
 
-def subm3d_adamw(tensors, count: int, step: AdamWStep, stream=None) -> None:
-    """Enqueue one step over `count` tensors (an array of subm3d_adamw_tensor)."""
-    st = lib.subm3d_adamw(tensors, int(count), ctypes.byref(step), _stream(stream))
+def adamw_tensors(rows):
+    """subm3d_adamw_tensor[] from one 8-tuple a tensor, in the fields' order: eight
+    64-bit words each.  (Plain words: filling ctypes structures takes several times as
+    long, and it is most of a small step's time.)"""
+    return array.array("q", [v for row in rows for v in row])
+
+
+# subm3d_adamw_step from its fields in order
+adamw_step = struct.Struct("=5dqQQiiiI").pack
+assert struct.calcsize("=5dqQQiiiI") == ctypes.sizeof(AdamWStep)
+assert ctypes.sizeof(AdamWTensor) == 64
+
+
+def subm3d_adamw(tensors, count: int, step: bytes, stream=None) -> None:
+    """Enqueue one step over `count` tensors (adamw_tensors(), adamw_step())."""
+    st = lib.subm3d_adamw(tensors.buffer_info()[0], count, step, _stream(stream))
     _check(st, "subm3d_adamw")
 
 

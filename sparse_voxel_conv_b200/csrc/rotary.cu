@@ -13,10 +13,12 @@
 // the nearest whole number (exact); the rest, within [-1/2, 1/2], goes through
 // sincospif.
 //
-// Bound by HBM: x is read and y written once.  A thread takes the P pairs of one
-// 16-byte load (two loads half a vector apart in the halves layout), computes
-// their cos and sin once and keeps them in registers over a run of the row's
-// heads; kUnroll heads are loaded before the first is stored.
+// Bound by HBM: x is read and y written once (131,072 x 24 of 36 x 128 bf16: 245 us,
+// 6.6 TB/s).  A thread takes the P pairs of one 16-byte load (two loads half a
+// vector apart in the halves layout), computes their cos and sin once, while its
+// first loads are on their way, and keeps them in registers over a run of the
+// row's heads.  With a head or two a row the angles bound it instead (131,072 x 1
+// x 64 bf16: 21 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -28,7 +30,7 @@ namespace subm3d {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;
+
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -48,11 +50,17 @@ template <typename T, int E>
 struct Part {
   T v[E];
   __device__ __forceinline__ void load(const T* p) {
-    if constexpr (sizeof(T) * E == 16)
-      *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(p);
-    else
+    if constexpr (sizeof(T) * E == 16) {
+      uint4 w;  // volatile: stays in front of the angles' arithmetic
+      asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                   : "l"(p)
+                   : "memory");
+      *reinterpret_cast<uint4*>(v) = w;
+    } else {
 #pragma unroll
       for (int i = 0; i < E; ++i) v[i] = p[i];
+    }
   }
   __device__ __forceinline__ void store(T* p) const {
     if constexpr (sizeof(T) * E == 16)
@@ -83,7 +91,11 @@ __device__ __forceinline__ void cos_sin(const RotaryArgs& a, const double* turns
     if (p < a.pairs) {
       const double at = p < e0 ? pos[0] : (p < e1 ? pos[1] : (p < e2 ? pos[2] : pos[3]));
       const double t = at * turns[p];
-      sincospif(2.0f * static_cast<float>(t - rint(t)), &s[i], &c[i]);
+      // the nearest whole number, by the rounding of a sum in [2^52, 2^53) (a
+      // conversion instruction runs at a fraction of the adds' rate)
+      constexpr double kWhole = 6755399441055744.0;  // 1.5 * 2^52
+      const double whole = __dadd_rn(__dadd_rn(t, kWhole), -kWhole);
+      sincospif(2.0f * static_cast<float>(t - whole), &s[i], &c[i]);
       if (a.inverse) s[i] = -s[i];
     }
   }
@@ -98,6 +110,10 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
   pdl_wait();
   __syncthreads();
   constexpr int E = HALVES ? P : 2 * P;
+  // heads loaded before the first is stored (twice the registers a head for halves: 33,331 x
+  // 5 x 72 fp32 17.2 us with 3, 19.7 with 4; 131,072 x 24 x 128 bf16 interleaved 243 with 4,
+  // 260 with 2)
+  constexpr int kUnroll = HALVES ? 3 : 4;
   const uint32_t half = a.head_dim / 2, slots = half / P, runs = a.runs, run = a.run_heads;
   const int64_t total = a.n * runs * slots;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
@@ -117,18 +133,22 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
       h0 = static_cast<uint32_t>(q - r * runs) * run;
     }
     const uint32_t h1 = min(h0 + run, static_cast<uint32_t>(a.heads));
-    float c[P], s[P];
-    cos_sin<P>(a, turns, r, slot * P, c, s);
     const T* x = static_cast<const T*>(a.x) + r * a.x_row + slot * E;
     T* y = static_cast<T*>(a.y) + r * a.y_row + slot * E;
-    for (uint32_t h = h0; h < h1; h += kUnroll) {
-      Part<T, E> lo[kUnroll], hi[HALVES ? kUnroll : 1];
+    Part<T, E> lo[kUnroll], hi[HALVES ? kUnroll : 1];
+    const auto load = [&](uint32_t h) {
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u)
         if (h + u < h1) {
           lo[u].load(x + (h + u) * a.x_head);
-          if (HALVES) hi[u].load(x + (h + u) * a.x_head + half);
+          if (HALVES) hi[HALVES ? u : 0].load(x + (h + u) * a.x_head + half);
         }
+    };
+    load(h0);  // on its way while the angles are computed
+    float c[P], s[P];
+    cos_sin<P>(a, turns, r, slot * P, c, s);
+    for (uint32_t h = h0; h < h1; h += kUnroll) {
+      if (h > h0) load(h);
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         if (h + u >= h1) continue;
@@ -157,7 +177,7 @@ cudaError_t launch(RotaryArgs a, int num_sms, cudaStream_t stream) {
   // compute, but a short call is spread over the device.
   const int64_t slots = a.head_dim / 2 / P;
   const int64_t want = static_cast<int64_t>(num_sms) * 2048;
-  const int64_t most_runs = (a.heads + kUnroll - 1) / kUnroll;
+  const int64_t most_runs = (a.heads + 3) / 4;
   int64_t runs = std::min(std::max<int64_t>(want / (a.n * slots), 1), most_runs);
   a.run_heads = static_cast<int32_t>((a.heads + runs - 1) / runs);
   a.runs = (a.heads + a.run_heads - 1) / a.run_heads;

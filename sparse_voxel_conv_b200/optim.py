@@ -19,6 +19,10 @@ _CODE, _SCALE = torch.float8_e4m3fn, torch.float8_e8m0fnu
 def _each(name, tensors, dtype, dev: int, sizes):
     """The addresses of a list that runs along the parameters, after a check of their
     number, type, device, sizes and layout."""
+    at = [t.data_ptr() for t in tensors
+          if t.dtype is dtype and t.get_device() == dev and t.is_contiguous()]
+    if len(at) == len(sizes) and [t.numel() for t in tensors] == sizes:
+        return at
     if len(tensors) != len(sizes):
         raise ValueError(f"{name} must have one tensor for each of {len(sizes)} parameters")
     for i, (t, n) in enumerate(zip(tensors, sizes)):
@@ -30,7 +34,6 @@ def _each(name, tensors, dtype, dev: int, sizes):
             raise ValueError(f"{name}[{i}] has the wrong number of elements")
         if not t.is_contiguous():
             raise ValueError(f"{name}[{i}] must be contiguous")
-    return [t.data_ptr() for t in tensors]
 
 
 def _scalar(t, name, dtype, dev: int):
@@ -93,7 +96,7 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0.9, 
         vs_at = _each("exp_avg_sq_scales", exp_avg_sq_scales, _SCALE, dev, blocks)
     elif exp_avg_scales is not None or exp_avg_sq_scales is not None:
         raise ValueError("32-bit moments have no scales")
-    step_at = lr_at = None
+    step_at = lr_at = 0
     if isinstance(step, torch.Tensor):
         step, step_at = 0, _scalar(step, "step", torch.int32, dev)
     if isinstance(lr, torch.Tensor):
@@ -101,9 +104,9 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0.9, 
     if stream is not None:
         _on_side_stream(stream)
     _abi.subm3d_adamw(
-        _abi.adamw_tensors(list(zip(p_at, g_at, m_at, v_at, ms_at, vs_at, w_at, sizes))), count,
-        _abi.AdamWStep(lr, betas[0], betas[1], eps, weight_decay, step, step_at, lr_at,
-                       _DTYPES[p_type], _DTYPES[g_type], 8 if bits8 else 32, seed & 0xFFFFFFFF),
+        _abi.adamw_tensors(zip(p_at, g_at, m_at, v_at, ms_at, vs_at, w_at, sizes)), count,
+        _abi.adamw_step(lr, betas[0], betas[1], eps, weight_decay, step, step_at, lr_at,
+                        _DTYPES[p_type], _DTYPES[g_type], 8 if bits8 else 32, seed & 0xFFFFFFFF),
         stream)
     _written(params)
     if masters is not None:
