@@ -288,9 +288,11 @@ def subm3d_layer_norm(x, n: int, channels: int, x_stride: int, dtype: int, weigh
                       affine_dtype: int, eps: float, act: int, y, mean, rstd,
                       stream=None) -> None:
     """Enqueue y = act(layer norm of x's rows); raises Subm3dError on an argument error."""
-    st = lib.subm3d_layer_norm(_ptr(x), n, channels, x_stride, dtype, _ptr(weight), _ptr(bias),
-                               affine_dtype, eps, act, _ptr(y), _ptr(mean), _ptr(rstd),
-                               _stream(stream))
+    st = lib.subm3d_layer_norm(x.data_ptr(), n, channels, x_stride, dtype,
+                               None if weight is None else weight.data_ptr(),
+                               None if bias is None else bias.data_ptr(), affine_dtype, eps, act,
+                               y.data_ptr(), None if mean is None else mean.data_ptr(),
+                               None if rstd is None else rstd.data_ptr(), _stream(stream))
     if st:
         _check(st, "subm3d_layer_norm")
 
@@ -321,11 +323,12 @@ def subm3d_rotary(x, x_row: int, x_head: int, n: int, heads: int, head_dim: int,
                   halves: bool, inverse: bool, y, y_row: int, y_head: int, stream=None) -> None:
     """Enqueue y = x turned by its rows' positions (axis_pairs: pairs per axis)."""
     pairs = _int32_array(tuple(axis_pairs))
-    st = lib.subm3d_rotary(_ptr(x), x_row, x_head, n, heads, head_dim, dtype, _ptr(positions),
-                           1 if positions_f32 else 0, pos_stride, len(axis_pairs), pairs, theta,
-                           1 if halves else 0, 1 if inverse else 0, _ptr(y), y_row, y_head,
-                           _stream(stream))
-    _check(st, "subm3d_rotary")
+    st = lib.subm3d_rotary(x.data_ptr(), x_row, x_head, n, heads, head_dim, dtype,
+                           positions.data_ptr(), 1 if positions_f32 else 0, pos_stride,
+                           len(axis_pairs), pairs, theta, 1 if halves else 0,
+                           1 if inverse else 0, y.data_ptr(), y_row, y_head, _stream(stream))
+    if st:
+        _check(st, "subm3d_rotary")
 
 
 class AdamWTensor(ctypes.Structure):

@@ -31,45 +31,48 @@ def _rows(t: torch.Tensor, name: str):
 
 
 def _affine(t, name: str, x_dtype, c: int, dev: int):
+    """A weight or bias vector, checked and contiguous (None stays None)."""
+    if t is None:
+        return None
     if t.dtype is not torch.float32 and t.dtype is not x_dtype:
         raise ValueError(f"{name} must be float32 or {x_dtype}, got {t.dtype}")
-    if t.shape != (c,):
+    if t.dim() != 1 or t.numel() != c:
         raise ValueError(f"{name} must have shape [{c}]")
-    _same_device(dev, name, t)
-    return t.contiguous()
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    return t if t.is_contiguous() else t.contiguous()
 
 
-def _affine_of(weight, bias, x_dtype, c: int, dev: int):
-    """(weight, bias, type code) checked."""
-    if weight is not None:
-        weight = _affine(weight, "weight", x_dtype, c, dev)
-    if bias is not None:
-        bias = _affine(bias, "bias", x_dtype, c, dev)
-        if weight is not None and weight.dtype is not bias.dtype:
-            raise ValueError("weight and bias must have one dtype")
-        return weight, bias, _DTYPES[bias.dtype]
-    return weight, bias, _DTYPES[x_dtype if weight is None else weight.dtype]
+def _affine_code(weight, bias, x_dtype) -> int:
+    if weight is None:
+        return _DTYPES[x_dtype if bias is None else bias.dtype]
+    if bias is not None and weight.dtype is not bias.dtype:
+        raise ValueError("weight and bias must have one dtype")
+    return _DTYPES[weight.dtype]
 
 
 def _codes(dtype, act):
-    if dtype not in _DTYPES:
-        raise ValueError(f"unsupported dtype {dtype}")
-    if act not in _ACTS:
-        raise ValueError(f"unknown activation {act!r}")
-    return _DTYPES[dtype], _ACTS[act]
+    try:
+        return _DTYPES[dtype], _ACTS[act]
+    except (KeyError, TypeError):
+        if dtype not in _DTYPES:
+            raise ValueError(f"unsupported dtype {dtype}") from None
+        raise ValueError(f"unknown activation {act!r}") from None
 
 
 def _norm(x, weight, bias, eps, act, out, stream, stats: bool):
-    dev = _device_of(x, "x")
-    if dev != _current_device():
-        with torch.cuda.device(dev):
+    dev = x.get_device()
+    if dev < 0 or dev != _current_device():
+        with torch.cuda.device(_device_of(x, "x")):
             return _norm(x, weight, bias, eps, act, out, stream, stats)
     x_dtype = x.dtype
     dtype, act_code = _codes(x_dtype, act)
     rows, stride = _rows(x, "x")
-    c = x.shape[-1]
+    c = rows.shape[-1]
     n = x.numel() // c
-    w, b, affine_dtype = _affine_of(weight, bias, x_dtype, c, dev)
+    w = _affine(weight, "weight", x_dtype, c, dev)
+    b = _affine(bias, "bias", x_dtype, c, dev)
+    affine_dtype = _affine_code(w, b, x_dtype)
     if out is None:
         y = torch.empty_like(x, memory_format=torch.contiguous_format)
     else:
@@ -98,6 +101,13 @@ def layer_norm_forward(x: torch.Tensor, weight: torch.Tensor | None = None,
     return _norm(x, weight, bias, eps, act, out, stream, True)
 
 
+def _stat(t, name: str, n: int, dev: int):
+    if t.dtype is not torch.float32 or t.numel() != n:
+        raise ValueError(f"{name} must be float32 with one value a row ({n})")
+    _same_device(dev, name, t)
+    return t if t.is_contiguous() else t.contiguous()
+
+
 def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
                         rstd: torch.Tensor, weight: torch.Tensor | None = None,
                         bias: torch.Tensor | None = None, act: str | None = None,
@@ -110,9 +120,9 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
     which of the three to compute; the others are None, and so are dweight without
     a weight and dbias without a bias.
     """
-    dev = _device_of(x, "x")
-    if dev != _current_device():
-        with torch.cuda.device(dev):
+    dev = x.get_device()
+    if dev < 0 or dev != _current_device():
+        with torch.cuda.device(_device_of(x, "x")):
             return layer_norm_backward(dy, x, mean, rstd, weight, bias, act, wanted, stream)
     x_dtype = x.dtype
     dtype, act_code = _codes(x_dtype, act)
@@ -122,15 +132,15 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
     dr, dy_stride = _rows(dy, "dy")
     c = x.shape[-1]
     n = x.numel() // c
-    w, b, affine_dtype = _affine_of(weight, bias, x_dtype, c, dev)
+    w = _affine(weight, "weight", x_dtype, c, dev)
+    b = _affine(bias, "bias", x_dtype, c, dev)
+    affine_dtype = _affine_code(w, b, x_dtype)
     _same_device(dev, "dy", dy)
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        if t.dtype is not torch.float32 or t.numel() != n:
-            raise ValueError(f"{name} must be float32 with one value a row ({n})")
-        _same_device(dev, name, t)
-    mean_c, rstd_c = mean.contiguous(), rstd.contiguous()
+    mean_c, rstd_c = _stat(mean, "mean", n, dev), _stat(rstd, "rstd", n, dev)
     want_dx, want_dw, want_db = wanted
-    dx = torch.empty_like(x, memory_format=torch.contiguous_format) if want_dx else None
+    dx = None
+    if want_dx:
+        dx = torch.empty_like(x, memory_format=torch.contiguous_format)
     dw = db = ws = None
     ws_bytes = 0
     if want_dw and w is not None:

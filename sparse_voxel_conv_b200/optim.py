@@ -66,9 +66,9 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0.9, 
     count = len(params)
     if count == 0:
         return
-    dev = _device_of(params[0], "params")
-    if dev != _current_device():
-        with torch.cuda.device(dev):
+    dev = params[0].get_device()
+    if dev < 0 or dev != _current_device():
+        with torch.cuda.device(_device_of(params[0], "params")):
             return adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas, eps,
                               weight_decay, masters, exp_avg_scales, exp_avg_sq_scales, seed,
                               stream)
@@ -119,8 +119,7 @@ class AdamW(torch.optim.Optimizer):
     state_bits: 32, or 8 for moments in about a byte each (see adamw_step).
     master_weights: keep float32 masters of bfloat16 parameters in the state;
     without them a bfloat16 weight loses every change below half its spacing.
-    seed: of the 8-bit rounding.  Parameters and gradients must be contiguous CUDA
-    tensors.  In a captured graph call adamw_step() with a device step instead.
+    seed: of the 8-bit rounding.  Parameters must be contiguous CUDA tensors.  In a captured graph call adamw_step() with a device step instead.
     """
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
@@ -177,7 +176,9 @@ class AdamW(torch.optim.Optimizer):
                 states = [st for _, st in members]
                 pick = lambda k: [st[k] for st in states]  # noqa: E731
                 bits8 = group["state_bits"] == 8
-                adamw_step(params, [p.grad for p in params], pick("exp_avg"), pick("exp_avg_sq"),
+                grads = [p.grad if p.grad.is_contiguous() else p.grad.contiguous()
+                         for p in params]
+                adamw_step(params, grads, pick("exp_avg"), pick("exp_avg_sq"),
                            key[-1] + 1, lr=group["lr"], betas=group["betas"], eps=group["eps"],
                            weight_decay=group["weight_decay"],
                            masters=pick("master") if key[3] else None,

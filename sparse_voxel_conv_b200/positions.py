@@ -18,9 +18,9 @@ __all__ = ["rotary", "VoxelRotary"]
 
 
 def _turn(x, positions, theta, axis_pairs, interleaved, inverse, out, stream):
-    dev = _device_of(x, "x")
-    if dev != _current_device():
-        with torch.cuda.device(dev):
+    dev = x.get_device()
+    if dev < 0 or dev != _current_device():
+        with torch.cuda.device(_device_of(x, "x")):
             return _turn(x, positions, theta, axis_pairs, interleaved, inverse, out, stream)
     dtype, shape = x.dtype, x.shape
     if dtype not in _DTYPES:
@@ -123,6 +123,6 @@ class VoxelRotary(torch.nn.Module):
         n, c = x.feats.shape
         if c % self.head_dim:
             raise ValueError(f"features must be whole heads of {self.head_dim} channels")
-        y = rotary(x.feats.view(n, c // self.head_dim, self.head_dim), x.coords[:, 1:], self.theta,
-                   self.axis_pairs, self.interleaved)
-        return x.replace(y.view(n, c))
+        heads = x.feats.reshape(n, c // self.head_dim, self.head_dim)
+        y = rotary(heads, x.coords[:, 1:], self.theta, self.axis_pairs, self.interleaved)
+        return x.replace(y.reshape(n, c))

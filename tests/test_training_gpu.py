@@ -223,3 +223,58 @@ def test_two_threads(S):
     assert not errors
     for p, q in zip(got, want):
         assert all(torch.equal(s, t) for s, t in zip(p, q))
+
+
+def test_first_call_is_a_captured_one():
+    """A fresh process whose first calls of the library are captured ones (kernels are loaded,
+    and given their shared memory, inside the capture)."""
+    import subprocess
+    import sys
+
+    code = """
+import torch, sparse_voxel_conv_b200 as S
+x = torch.randn(300, 128, device='cuda').bfloat16()
+w, b = torch.ones(128, device='cuda'), torch.zeros(128, device='cuda')
+pos = torch.zeros(300, 3, dtype=torch.int32, device='cuda')
+m, v, g = (torch.zeros(128, device='cuda') for _ in range(3))
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    y, mean, rstd = S.layer_norm_forward(x, w, b, act='silu')
+    grads = S.layer_norm_backward(y, x, mean, rstd, w, b, act='silu')
+    z = S.rotary(y.view(300, 2, 64), pos)
+    S.adamw_step([w], [g], [m], [v], 1, lr=0.0)
+graph.replay()
+torch.cuda.synchronize()
+want, m1, r1 = S.layer_norm_forward(x, w, b, act='silu')
+assert torch.equal(y, want) and torch.equal(z.view(300, 128), y)
+assert all(torch.equal(p, q) for p, q in zip(grads, S.layer_norm_backward(y, x, m1, r1, w, b, act='silu')))
+"""
+    p = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0, p.stdout + p.stderr
+
+
+def test_without_autograd_modes(S):
+    """Under inference_mode and no_grad, with out= and in place."""
+    x = torch.randn(100, 64, device="cuda")
+    pos = torch.randint(0, 9, (100, 3), device="cuda", dtype=torch.int32)
+    want, turned = S.layer_norm(x), S.rotary(x, pos)
+    for mode in (torch.inference_mode, torch.no_grad):
+        with mode():
+            p = x.clone()
+            assert torch.equal(S.layer_norm(p, out=p), want) and torch.equal(p, want)
+            q = x.clone()
+            assert torch.equal(S.rotary(q, pos, out=q), turned)
+            w, g, m, v = (torch.ones(8, device="cuda") for _ in range(4))
+            S.adamw_step([w], [g], [m], [v], 1)
+            assert torch.isfinite(w).all()
+
+
+def test_gradients_that_are_not_contiguous(S):
+    """The optimizer takes a gradient of any layout."""
+    a, b = (torch.nn.Parameter(torch.ones(6, 8, device="cuda")) for _ in range(2))
+    g = torch.randn(8, 6, device="cuda")
+    a.grad, b.grad = g.t(), g.t().contiguous()
+    S.AdamW([a]).step()
+    S.AdamW([b]).step()
+    assert torch.equal(a, b)
