@@ -365,7 +365,7 @@ __device__ __forceinline__ void step_elements(const AdamWStep& a, const Hyper& h
 }
 
 template <bool BITS8, bool PARAM_BF16, bool GRAD_BF16, int CAP>
-__global__ void __launch_bounds__(kThreads, BITS8 ? 6 : 5)
+__global__ void __launch_bounds__(kThreads, 4)
     adamw_kernel(const __grid_constant__ AdamWStep a, const __grid_constant__ AdamWList<CAP> l) {
   pdl_wait();
   const Hyper h = hyper_of(a);

@@ -256,7 +256,9 @@ cudaError_t launch_join(const LayerNormGradArgs& a, int chunks, cudaStream_t str
 // walk over the rows with their columns' weights in registers.  Each lane copies its
 // own part of the rows ahead into its own shared-memory slots (cp.async): no
 // barrier, and the bytes in flight do not cost registers, which are what limits the
-// warps on an SM.
+// warps on an SM.  Single-element loads go to registers instead, one row ahead: as
+// copies they are twice as many shared-memory operations as the row has elements
+// (50,021 x 203 fp32: 18.3 us by copies, 15.9 by loads).
 
 // Rows a lane has under way, its present one included.  More cost shared memory and
 // gain nothing (gradient at 329,839 x 128 bf16: 43.3 us with 3, 44.3 with 4); 64-byte
@@ -268,11 +270,14 @@ constexpr int kMaxRowWarps = 16;  // of a team: rows up to 16 * 32 * 16 = 8,192 
 // Rows are counted in 32 bits, some strides of all teams beyond the last one included.
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - (1 << 20);
 constexpr int kFewestLanes = 4;   // of a team: 16 bytes of 64 channels a lane and load
-// Registers: 80 a thread forward (768 threads an SM), 128 for the gradients (512).  A
-// forward block has up to 256 threads, or one wider team; the gradient's blocks fill an
-// SM each, so that few partial sums are left to join.
-constexpr int kRowRegisters = 80, kRowThreads = 768, kRowBlock = 256;
-constexpr int kGradThreads = 512;
+// Registers of a thread and threads of an SM: forward as many threads as hold their
+// elements of a row without spilling (single-element loads hold half as many), the
+// gradient 128 registers.  A forward block has up to kRowBlock threads, or one wider
+// team; the gradient's blocks fill an SM each, so that few partial sums are left to
+// join (16,384 x 1,536 bf16: 35.7 us, 40.3 with two blocks an SM and a slower join).
+constexpr int row_registers(int e) { return e > 1 ? 80 : 64; }
+constexpr int row_threads(int e) { return e > 1 ? 768 : 1024; }
+constexpr int kRowBlock = 256, kGradThreads = 512;
 
 using f2 = unsigned long long;  // two fp32 values
 __device__ __forceinline__ f2 f2_set(float v) { return f2_pack(v, v); }
@@ -397,14 +402,13 @@ __device__ __forceinline__ uint32_t kept(uint32_t v) {
   return v;
 }
 
-// A lane's parts of the rows ahead.  Parts of 4 or 16 bytes are copied into the
+// A lane's parts of the rows ahead.  Parts of several elements are copied into the
 // lane's own shared-memory slots (S stages, kStage bytes apart; a warp's slots lie
-// together, [S][V][32] parts); single bf16 elements (odd widths) are held in
-// registers, one row ahead.
+// together, [S][V][32] parts); single elements are held in registers, one row ahead.
 template <typename T, int E, int V, int S>
 struct Ahead {
   static constexpr int kBytes = static_cast<int>(sizeof(T)) * E;
-  static constexpr bool kAsync = kBytes >= 4;
+  static constexpr bool kAsync = E > 1;
   static constexpr int N = V * E;
   static constexpr int kFront = kAsync ? S - 1 : 1;  // rows on their way
   const char* src;  // the lane's first vector of row 0
@@ -445,9 +449,16 @@ struct Ahead {
     for (int k = 0; k < V; ++k) {
       const char* p = row + k * t.step * kBytes;
       if constexpr (!kAsync) {
-        uint16_t h = 0;
-        if (live && on[k]) asm volatile("ld.global.b16 %0, [%1];" : "=h"(h) : "l"(p));
-        held[k] = h;
+        held[k] = 0u;
+        if (live && on[k]) {
+          if constexpr (kBytes == 2) {
+            uint16_t h;
+            asm volatile("ld.global.b16 %0, [%1];" : "=h"(h) : "l"(p));
+            held[k] = h;
+          } else {
+            asm volatile("ld.global.b32 %0, [%1];" : "=r"(held[k]) : "l"(p));
+          }
+        }
       } else {
         const uint32_t dst = mine + at + k * 32 * kBytes;
         if constexpr (kBytes == 16)
@@ -568,7 +579,7 @@ __device__ __forceinline__ void load_affine(f2 (&w)[V * E / 2], const void* p, b
 }
 
 template <typename T, int E, int V, int ACT, int LANES>
-__global__ void __maxnreg__(kRowRegisters) norm_row_kernel(LayerNormArgs a, int team_lanes) {
+__global__ void __maxnreg__(row_registers(E)) norm_row_kernel(LayerNormArgs a, int team_lanes) {
   constexpr bool WIDE = LANES == 0;
   const int lanes = WIDE ? team_lanes : LANES;
   // warps' sums and squares, two buffers in turn: one is written again only behind the
@@ -910,7 +921,7 @@ cudaError_t launch_norm_rows(const LayerNormArgs& a, const RowPlan& p, int num_s
   constexpr auto kernel = norm_row_kernel<T, E, V, ACT, LANES>;
   const cudaError_t e = allow_smem<kernel>(smem);
   if (e != cudaSuccess) return e;
-  const int64_t blocks = blocks_for(p.lanes, threads, a.n, kRowThreads, num_sms, 0x7FFFFFFF);
+  const int64_t blocks = blocks_for(p.lanes, threads, a.n, row_threads(E), num_sms, 0x7FFFFFFF);
   return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(threads), smem, stream, a,
                     p.lanes);
 }
