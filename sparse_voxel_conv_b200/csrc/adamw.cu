@@ -17,8 +17,14 @@
 // zero: the next step divides by it.  A block that holds an infinity or a NaN
 // gets the scale 255 (NaN): all its 32 elements are NaN from then on.
 //
-// Bound by HBM.  A thread takes 8 consecutive elements: 16-byte accesses, and a block
-// of 32 elements is four lanes', whose largest magnitude two shuffles find.
+// Bound by HBM: 28 bytes an element with fp32 weights and 32-bit moments (28.3 M
+// elements 119 us, 6.65 TB/s, the copy rate), 18.1 with bf16 weights, fp32 gradients
+// and masters and 8-bit moments (56.6 M elements 158 us at full clock, 6.5 TB/s; 172
+// in a sustained run, whose power lowers the clock: its 69 instructions an element
+// count).  A thread takes 8 consecutive elements: 16-byte accesses, and a block of 32
+// elements is four lanes', whose largest magnitude two shuffles find.  Arithmetic on
+// pairs (f32x2).  Four blocks of 256 threads an SM: with five or six the registers
+// spill (178 us), with two groups of elements a thread fewer loads overlap (195).
 //
 // The moments' products and sums are rounded one by one (no fma), so that the
 // states are the same bits as the formula in elementary fp32 operations gives.

@@ -145,6 +145,31 @@ def _check_8_bits(x, code, scale, positive):
     assert ok.all()
 
 
+@pytest.mark.parametrize("n", [1, 31, 32, 33, 2047, 2049, 100_003])
+def test_codes_bit_for_bit(S, n):
+    """The stored codes and scales are the documented rounding of the moments, with the
+    documented random bits; gradients over many powers of two, so that codes of every
+    size, subnormal ones among them, occur."""
+    st = Set([5, n], F32, F32, 8, False, 20)
+    for t in (1, 2, 70_000):
+        g = [torch.randn(k, device="cuda", generator=st.g) * torch.exp2(
+            torch.randint(-20, 3, (k,), device="cuda", generator=st.g).float()) for k in (5, n)]
+        st.grads = g
+        old = [st.values(i) for i in range(2)]
+        st.step(S, t, seed=99)
+        for i, k in enumerate((5, n)):
+            m, v = _moments_fp32(old[i][0], old[i][1] * old[i][1], g[i], HYPER["betas"])
+            bits = R.random_bits(torch.arange(k, device="cuda"), 99, t, i)
+            for x, low, code, scale, root in ((m, bits & 0xFFFF, st.m[i], st.ms[i], False),
+                                              (v.sqrt(), bits >> 16, st.v[i], st.vs[i], True)):
+                want, want_scale = R.e4m3_blocks(x, low, root)
+                assert torch.equal(scale.view(torch.uint8), want_scale)
+                got = code.view(torch.uint8)
+                # (the sign of a zero that a negative moment was rounded to is free)
+                same = (got == want) | ((got & 127) + (want & 127) == 0)
+                assert same.all(), (n, t, int((~same).sum()))
+
+
 def test_rounding_has_no_bias(S):
     """Over 400 seeds the mean of each stored moment is its value: within 5.5 standard
     deviations of a step's fair split for each of 4,096 elements (a fixed set of seeds:

@@ -143,3 +143,44 @@ def check(got, want, bound, what=""):
         i = int(over.argmax())
         raise AssertionError(f"{what}: {int((over > 0).sum())} of {over.numel()} beyond the bound; worst at {i}: "
                              f"{got.flatten()[i]!r} for {want.flatten()[i]!r} +- {bound.expand_as(want).flatten()[i]!r}")
+
+
+def _stir(x):
+    x = x ^ (x >> 16)
+    x = (x * 0x9E3779B1) & 0xFFFFFFFF
+    x = x ^ (x >> 15)
+    x = (x * 0xBB67AE85) & 0xFFFFFFFF
+    return x ^ (x >> 16)
+
+
+def random_bits(i, seed, step, place):
+    """The 32 random bits of elements i (int64) of the tensor at `place` in the call."""
+    k1 = _stir((seed + 0x9E3779B9 * step) & 0xFFFFFFFF)
+    k2 = _stir((k1 + 0xBB67AE85 * (place + 1)) & 0xFFFFFFFF)
+    x = ((i & 0xFFFFFFFF) + (i >> 32) * 0x3C6EF373 + k1) & 0xFFFFFFFF
+    x = x ^ (x >> 16)
+    x = ((x * 0x9E3779B1) & 0xFFFFFFFF) ^ k2
+    x = x ^ (x >> 15)
+    x = (x * 0xBB67AE85) & 0xFFFFFFFF
+    return x ^ (x >> 16)
+
+
+def e4m3_blocks(x, low, root):
+    """(code bytes, scale bytes) of x (fp32, whole blocks of 32 but the last) with the 16-bit
+    random numbers `low`: the spacing's share in units of 2^-16, plus half a unit, added
+    before the cut.  In 64 bits, where every step is exact."""
+    n = x.numel()
+    mag = x.double().abs()
+    top = torch.nn.functional.pad(mag, (0, -n % 32)).view(-1, 32).amax(1)
+    mant, e = torch.frexp(top)                      # top = mant 2^e, mant in [1/2, 1)
+    k = torch.where(mant > 0.875, e - 8, e - 9)     # the smallest k with top <= 448 2^k = 0.875 2^(k + 9)
+    k = torch.where(top > 0, k, -127).clamp(min=-127)
+    y = mag * torch.exp2(-k.double()).repeat_interleave(32)[:n]
+    gap = torch.exp2(torch.floor(torch.log2(y.clamp(min=2.0 ** -6)))) / 8
+    # fp32 words have 2^20 values between two codes: the cut sees x's share rounded to that
+    share = torch.floor(y / gap * 2 ** 20)
+    y = torch.floor((share + low.double() * 16 + 8) / 2 ** 20) * gap
+    if root:
+        y = torch.where(x > 0, y.clamp(min=2.0 ** -9), y)
+    code = torch.where(x < 0, -y, y).float().to(torch.float8_e4m3fn).view(torch.uint8)
+    return code, (k + 127).to(torch.uint8)
