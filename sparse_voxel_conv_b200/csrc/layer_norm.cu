@@ -571,16 +571,40 @@ __device__ __forceinline__ void team_barrier(const Team& t) {
 }
 
 // A lane's columns of a weight or bias vector; `none` without one, 0 behind the row.
+// Vectors that start on 16 bytes are read in 16-byte loads (they are on the way to a
+// block's first row).
 template <int E, int V>
 __device__ __forceinline__ void load_affine(f2 (&w)[V * E / 2], const void* p, bool bf16,
                                             float none, const Team& t, int vecs) {
+  const bool whole = reinterpret_cast<uintptr_t>(p) % 16 == 0;
   float v[V * E];
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     const int64_t c = static_cast<int64_t>(t.first + k * t.step) * E;
+    const bool on = t.first + k * t.step < vecs;
 #pragma unroll
-    for (int i = 0; i < E; ++i)
-      v[k * E + i] = t.first + k * t.step < vecs ? (p ? affine_at(p, bf16, c + i) : none) : 0.0f;
+    for (int i = 0; i < E; ++i) v[k * E + i] = on ? none : 0.0f;
+    if (!p || !on) continue;
+    if (E % 4 == 0 && whole && !bf16) {
+      const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + c);
+#pragma unroll
+      for (int i = 0; i < E / 4; ++i) {
+        const float4 f = q[i];
+        v[k * E + 4 * i] = f.x;
+        v[k * E + 4 * i + 1] = f.y;
+        v[k * E + 4 * i + 2] = f.z;
+        v[k * E + 4 * i + 3] = f.w;
+      }
+    } else if (E == 8 && whole) {
+      const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + c);
+      const uint32_t words[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        v[k * E + i] = __uint_as_float(i % 2 ? words[i / 2 % 4] & 0xFFFF0000u : words[i / 2 % 4] << 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[k * E + i] = affine_at(p, bf16, c + i);
+    }
   }
 #pragma unroll
   for (int i = 0; i < V * E; i += 2) w[i / 2] = f2_pack(v[i], v[i + 1]);
