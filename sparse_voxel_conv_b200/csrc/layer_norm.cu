@@ -32,8 +32,13 @@
 
 namespace subm3d {
 
-// Blocks that leave partial column sums: four on each of 148 SMs, fewer for few rows.
-int64_t layer_norm_chunks(int64_t n) { return std::min<int64_t>((n + 15) / 16, 592); }
+constexpr int kMaxRowElements = 8192;  // of a row kernel
+
+// The most blocks that leave partial column sums: four on each of 148 SMs.  Fewer for
+// the widest rows, whose sums take the more room the fewer the rows.
+int64_t layer_norm_chunks(int64_t n, int32_t channels) {
+  return std::min<int64_t>(channels <= kMaxRowElements ? n : (n + 63) / 64, 592);
+}
 
 namespace {
 
@@ -274,7 +279,8 @@ cudaError_t launch_join(const LayerNormGradArgs& a, int chunks, cudaStream_t str
 constexpr int kRowStages = 4;
 template <typename T, int E, int V>
 constexpr int kGradStages = sizeof(T) * E * V >= 64 ? 2 : 3;
-constexpr int kMaxRowWarps = 16;  // of a team: rows up to 16 * 32 * 16 = 8,192 elements
+constexpr int kMaxRowWarps = 16;  // of a team: 16 * 32 lanes of 16 elements
+static_assert(kMaxRowWarps * 32 * 16 == kMaxRowElements, "");
 // Rows are counted in 32 bits, some strides of all teams beyond the last one included.
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - (1 << 20);
 constexpr int kFewestLanes = 4;   // of a team: 16 bytes of 64 channels a lane and load
@@ -857,29 +863,45 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   float* sums = reinterpret_cast<float*>(ring);
   const int groups = WIDE ? blockDim.x / lanes : blockDim.x / 32;
   if (t.sub == 0) {
-    float* mine = sums + (WIDE ? t.id : static_cast<int>(threadIdx.x) / 32) * 2 * a.c;
+    float* mine = sums + (WIDE ? t.id : static_cast<int>(threadIdx.x) / 32) * 2 * a.c +
+                  t.first * E;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (!ax.on[i / E]) continue;
-      float lo, hi;
-      const int c = (t.first + i / E * t.step) * E + i % E;
-      f2_unpack(dw[i / 2], lo, hi);
-      mine[c] = i % 2 ? hi : lo;
-      f2_unpack(db[i / 2], lo, hi);
-      mine[a.c + c] = i % 2 ? hi : lo;
+    for (int k = 0; k < V; ++k) {
+      if (!ax.on[k]) continue;
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const int e = k * E + i, c = k * t.step * E + i;
+        float lo, hi;
+        f2_unpack(dw[e / 2], lo, hi);
+        mine[c] = e % 2 ? hi : lo;
+        f2_unpack(db[e / 2], lo, hi);
+        mine[a.c + c] = e % 2 ? hi : lo;
+      }
     }
   }
   __syncthreads();
-  float* partial = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.c;
-  for (int c = threadIdx.x; c < 2 * a.c; c += blockDim.x) {
-    float sum = sums[c];
-    for (int k = 1; k < groups; ++k) sum += sums[k * 2 * a.c + c];
-    if (gridDim.x > 1) {
-      partial[c] = sum;
-    } else {
-      float* out = c < a.c ? a.dweight : a.dbias;
-      if (out) out[c < a.c ? c : c - a.c] = sum;
+  const int group = 2 * a.c, step = blockDim.x;
+  // the groups' sums of `count` columns from `first` on, four columns under way
+  const auto add_up = [&](float* out, int first, int count) {
+    const float* from = sums + first;
+    for (int c = threadIdx.x; c < count; c += 4 * step) {
+      float sum[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum[j] = c + j * step < count ? from[c + j * step] : 0.0f;
+      for (int k = 1; k < groups; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (c + j * step < count) sum[j] += from[k * group + c + j * step];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c + j * step < count) out[c + j * step] = sum[j];
     }
+  };
+  if (gridDim.x > 1) {
+    add_up(a.partial + static_cast<int64_t>(blockIdx.x) * group, 0, group);
+  } else {
+    if (a.dweight) add_up(a.dweight, 0, a.c);
+    if (a.dbias) add_up(a.dbias, a.c, a.c);
   }
 }
 
@@ -973,7 +995,7 @@ cudaError_t launch_grad_rows(const LayerNormGradArgs& a, const RowPlan& p, int n
   cudaError_t e = allow_smem<kernel>(smem);
   if (e != cudaSuccess) return e;
   const int64_t blocks =
-      blocks_for(p.lanes, threads, a.n, kGradThreads, num_sms, layer_norm_chunks(a.n));
+      blocks_for(p.lanes, threads, a.n, kGradThreads, num_sms, layer_norm_chunks(a.n, a.c));
   e = launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(threads), smem, stream, a,
                  p.lanes);
   if (e != cudaSuccess || !a.partial || blocks == 1) return e;
@@ -1032,7 +1054,7 @@ cudaError_t launch_layer_norm_grad(const LayerNormGradArgs& in, int num_sms, cud
     if (e != cudaSuccess) return e;
   }
   if (!a.dweight && !a.dbias) return e;
-  const int64_t chunks = layer_norm_chunks(a.n);
+  const int64_t chunks = layer_norm_chunks(a.n, a.c);
   const int64_t rows = (a.n + chunks - 1) / chunks;
   const unsigned cols = static_cast<unsigned>((a.c + 31) / 32);
   const dim3 grid(cols, static_cast<unsigned>(chunks));

@@ -547,7 +547,7 @@ subm3d_status subm3d_layer_norm(const void* x, int64_t n, int32_t channels, int6
 
 size_t subm3d_layer_norm_workspace_bytes(int64_t n, int32_t channels) {
   if (n < 0 || channels < 1 || channels > kMaxNormChannels) return 0;
-  return static_cast<size_t>(subm3d::layer_norm_chunks(n)) * 2 * channels * 4;
+  return static_cast<size_t>(subm3d::layer_norm_chunks(n, channels)) * 2 * channels * 4;
 }
 
 subm3d_status subm3d_layer_norm_backward(
