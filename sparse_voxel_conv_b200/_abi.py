@@ -306,11 +306,17 @@ def subm3d_layer_norm_backward(dy, dy_stride: int, x, x_stride: int, n: int, cha
                                dx, dweight, dbias, workspace, workspace_bytes: int,
                                stream=None) -> None:
     """Enqueue the layer norm's gradients (dx, dweight, dbias may each be None)."""
-    st = lib.subm3d_layer_norm_backward(_ptr(dy), dy_stride, _ptr(x), x_stride, n, channels,
-                                        dtype, _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(bias),
-                                        affine_dtype, act, _ptr(dx), _ptr(dweight), _ptr(dbias),
-                                        _ptr(workspace), workspace_bytes, _stream(stream))
-    _check(st, "subm3d_layer_norm_backward")
+    st = lib.subm3d_layer_norm_backward(dy.data_ptr(), dy_stride, x.data_ptr(), x_stride, n,
+                                        channels, dtype, mean.data_ptr(), rstd.data_ptr(),
+                                        None if weight is None else weight.data_ptr(),
+                                        None if bias is None else bias.data_ptr(), affine_dtype,
+                                        act, None if dx is None else dx.data_ptr(),
+                                        None if dweight is None else dweight.data_ptr(),
+                                        None if dbias is None else dbias.data_ptr(),
+                                        None if workspace is None else workspace.data_ptr(),
+                                        workspace_bytes, _stream(stream))
+    if st:
+        _check(st, "subm3d_layer_norm_backward")
 
 
 @functools.lru_cache(maxsize=64)

@@ -295,7 +295,7 @@ struct RotaryArgs {
   int32_t run_heads = 0, runs = 0;  // heads a thread takes, runs of them (set by the launch)
   int32_t axis_pairs[kRotaryMaxAxes] = {};
   bool bf16 = false, pos_f32 = false, halves = false, inverse = false;
-  double turns[kRotaryMaxPairs] = {};
+  double turns[kRotaryMaxPairs];
 };
 cudaError_t launch_rotary(const RotaryArgs& a, int num_sms, cudaStream_t stream);
 

@@ -498,6 +498,27 @@ int64_t rows_bytes(int64_t n, int64_t stride, int64_t width, size_t esz) {
   return n > 0 ? ((n - 1) * stride + width) * static_cast<int64_t>(esz) : 0;
 }
 
+// Turns per unit of position of each pair.  The thread's last table is kept, told by the
+// numbers that it was made from: its exponentials are a microsecond of a short call.
+struct RotaryTable {
+  double theta = 0.0;
+  int32_t axis_pairs[subm3d::kRotaryMaxAxes] = {};
+  double turns[subm3d::kRotaryMaxPairs];
+};
+const RotaryTable& rotary_table(double theta, const int32_t (&axis_pairs)[subm3d::kRotaryMaxAxes]) {
+  static thread_local RotaryTable t;
+  if (t.theta == theta && std::equal(axis_pairs, axis_pairs + subm3d::kRotaryMaxAxes, t.axis_pairs))
+    return t;
+  const double log_theta = std::log(theta);
+  int used = 0;
+  for (int32_t pairs : axis_pairs)
+    for (int32_t j = 0; j < pairs; ++j)
+      t.turns[used++] = std::exp(-log_theta * j / pairs) / 6.283185307179586476925;
+  t.theta = theta;
+  std::copy(axis_pairs, axis_pairs + subm3d::kRotaryMaxAxes, t.axis_pairs);
+  return t;
+}
+
 subm3d_status of(cudaError_t e) { return e == cudaSuccess ? SUBM3D_OK : SUBM3D_E_CUDA; }
 
 }  // namespace
@@ -624,14 +645,9 @@ subm3d_status subm3d_rotary(const void* x, int64_t x_row, int64_t x_head, int64_
       x_row < 0 || x_head < 0 || y_row < 0 || y_head < 0 || pos_stride < 0)
     return SUBM3D_E_INVALID;
   if (head_dim % 2 != 0 || head_dim / 2 > subm3d::kRotaryMaxPairs) return SUBM3D_E_UNSUPPORTED;
-  subm3d::RotaryArgs a;
   int64_t used = 0;
-  const double log_theta = std::log(theta);
   for (int i = 0; i < axes; ++i) {
     if (axis_pairs[i] < 0 || axis_pairs[i] > head_dim / 2 - used) return SUBM3D_E_INVALID;
-    a.axis_pairs[i] = axis_pairs[i];
-    for (int j = 0; j < axis_pairs[i]; ++j)
-      a.turns[used + j] = std::exp(-log_theta * j / axis_pairs[i]) / 6.283185307179586476925;
     used += axis_pairs[i];
   }
   if (n == 0 || heads == 0) return SUBM3D_OK;
@@ -654,6 +670,10 @@ subm3d_status subm3d_rotary(const void* x, int64_t x_row, int64_t x_head, int64_
                   span(positions, ((n - 1) * pos_stride + axes) * 4, false),
                   span(y, reach(y_row, y_head, head_dim, esz), true)};
   if (clash(spans, 3)) return SUBM3D_E_INVALID;
+  subm3d::RotaryArgs a;
+  std::copy(axis_pairs, axis_pairs + axes, a.axis_pairs);
+  const RotaryTable& table = rotary_table(theta, a.axis_pairs);
+  std::copy(table.turns, table.turns + used, a.turns);
   a.x = x;
   a.y = y;
   a.pos = positions;

@@ -104,7 +104,8 @@ def layer_norm_forward(x: torch.Tensor, weight: torch.Tensor | None = None,
 def _stat(t, name: str, n: int, dev: int):
     if t.dtype is not torch.float32 or t.numel() != n:
         raise ValueError(f"{name} must be float32 with one value a row ({n})")
-    _same_device(dev, name, t)
+    if t.get_device() != dev:
+        _same_device(dev, name, t)
     return t if t.is_contiguous() else t.contiguous()
 
 
@@ -124,29 +125,29 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
     if dev < 0 or dev != _current_device():
         with torch.cuda.device(_device_of(x, "x")):
             return layer_norm_backward(dy, x, mean, rstd, weight, bias, act, wanted, stream)
-    x_dtype = x.dtype
+    x_dtype, shape = x.dtype, x.shape
     dtype, act_code = _codes(x_dtype, act)
-    if dy.shape != x.shape or dy.dtype != x_dtype:
+    if dy.shape != shape or dy.dtype is not x_dtype:
         raise ValueError("dy must have x's shape and dtype")
+    if dy.get_device() != dev:
+        _same_device(dev, "dy", dy)
     xr, x_stride = _rows(x, "x")
     dr, dy_stride = _rows(dy, "dy")
-    c = x.shape[-1]
+    c = shape[-1]
     n = x.numel() // c
-    w = _affine(weight, "weight", x_dtype, c, dev)
-    b = _affine(bias, "bias", x_dtype, c, dev)
+    w = None if weight is None else _affine(weight, "weight", x_dtype, c, dev)
+    b = None if bias is None else _affine(bias, "bias", x_dtype, c, dev)
     affine_dtype = _affine_code(w, b, x_dtype)
-    _same_device(dev, "dy", dy)
     mean_c, rstd_c = _stat(mean, "mean", n, dev), _stat(rstd, "rstd", n, dev)
     want_dx, want_dw, want_db = wanted
-    dx = None
+    dx = dw = db = ws = None
     if want_dx:
         dx = torch.empty_like(x, memory_format=torch.contiguous_format)
-    dw = db = ws = None
-    ws_bytes = 0
     if want_dw and w is not None:
         dw = mean_c.new_empty(c)
     if want_db and b is not None:
         db = mean_c.new_empty(c)
+    ws_bytes = 0
     if dw is not None or db is not None:
         ws_bytes = _abi.subm3d_layer_norm_workspace_bytes(n, c)
         ws = mean_c.new_empty(ws_bytes // 4)
