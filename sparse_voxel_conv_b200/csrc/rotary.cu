@@ -14,10 +14,10 @@
 // sincospif.
 //
 // Bound by HBM: x is read and y written once (131,072 x 24 of 36 x 128 bf16: 245 us,
-// 6.6 TB/s).  A thread takes the P pairs of one 16-byte load (two loads half a
-// vector apart in the halves layout), computes their cos and sin once, while its
-// first loads are on their way, and keeps them in registers over a run of the
-// row's heads.  With a head or two a row the angles bound it instead (131,072 x 1
+// 6.6 TB/s).  A thread takes the P pairs of one load, as wide as the head vectors'
+// alignment allows up to 16 bytes (two loads half a vector apart in the halves
+// layout), computes their cos and sin once, while its first loads are on their way,
+// and keeps them in registers over a run of the row's heads.  With a head or two a row the angles bound it instead (131,072 x 1
 // x 64 bf16: 21 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -45,29 +45,50 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
   return __float2bfloat16_rn(v);
 }
 
-// E elements of T in one access: 16 bytes, or single ones.
-template <typename T, int E>
+// E elements of T: in one access of 2 to 16 bytes (WHOLE), or element by element.
+// Volatile loads: they stay in front of the angles' arithmetic.
+template <typename T, int E, bool WHOLE>
 struct Part {
-  T v[E];
+  static constexpr int kBytes = static_cast<int>(sizeof(T)) * E;
+  alignas(kBytes) T v[E];
   __device__ __forceinline__ void load(const T* p) {
-    if constexpr (sizeof(T) * E == 16) {
-      uint4 w;  // volatile: stays in front of the angles' arithmetic
+    if constexpr (!WHOLE) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] = p[i];
+    } else if constexpr (kBytes == 16) {
+      uint4 w;
       asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
                    : "l"(p)
                    : "memory");
       *reinterpret_cast<uint4*>(v) = w;
+    } else if constexpr (kBytes == 8) {
+      uint2 w;
+      asm volatile("ld.global.v2.b32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "l"(p) : "memory");
+      *reinterpret_cast<uint2*>(v) = w;
+    } else if constexpr (kBytes == 4) {
+      uint32_t w;
+      asm volatile("ld.global.b32 %0, [%1];" : "=r"(w) : "l"(p) : "memory");
+      *reinterpret_cast<uint32_t*>(v) = w;
     } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) v[i] = p[i];
+      uint16_t w;
+      asm volatile("ld.global.b16 %0, [%1];" : "=h"(w) : "l"(p) : "memory");
+      *reinterpret_cast<uint16_t*>(v) = w;
     }
   }
   __device__ __forceinline__ void store(T* p) const {
-    if constexpr (sizeof(T) * E == 16)
-      *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(v);
-    else
+    if constexpr (!WHOLE) {
 #pragma unroll
       for (int i = 0; i < E; ++i) p[i] = v[i];
+    } else if constexpr (kBytes == 16) {
+      *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(v);
+    } else if constexpr (kBytes == 8) {
+      *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(v);
+    } else if constexpr (kBytes == 4) {
+      *reinterpret_cast<uint32_t*>(p) = *reinterpret_cast<const uint32_t*>(v);
+    } else {
+      *p = v[0];
+    }
   }
 };
 
@@ -101,19 +122,24 @@ __device__ __forceinline__ void cos_sin(const RotaryArgs& a, const double* turns
   }
 }
 
+// Heads loaded before the first is stored (twice the registers a head for halves).
+// 16-byte parts: 33,331 x 5 x 72 fp32 halves 17.2 us with 3, 19.7 with 4; 131,072 x 24 x
+// 128 bf16 interleaved 243 with 4, 260 with 2.  Narrower parts take more.
+__host__ __device__ constexpr int unroll_of(int bytes, bool halves) {
+  if (halves) return bytes == 16 ? 3 : 4;
+  return bytes == 16 ? 4 : (bytes == 8 ? 6 : 8);
+}
+
 // Items: (row, run of heads, P pairs).  HALVES: the pairs' second elements lie half a
 // vector behind the first ones.
-template <typename T, int P, bool HALVES>
+template <typename T, int P, bool HALVES, bool WHOLE>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a) {
   extern __shared__ double turns[];
   for (int i = threadIdx.x; i < a.pairs; i += kThreads) turns[i] = a.turns[i];
   pdl_wait();
   __syncthreads();
   constexpr int E = HALVES ? P : 2 * P;
-  // heads loaded before the first is stored (twice the registers a head for halves: 33,331 x
-  // 5 x 72 fp32 17.2 us with 3, 19.7 with 4; 131,072 x 24 x 128 bf16 interleaved 243 with 4,
-  // 260 with 2)
-  constexpr int kUnroll = HALVES ? 3 : 4;
+  constexpr int kUnroll = unroll_of(static_cast<int>(sizeof(T)) * E, HALVES);
   const uint32_t half = a.head_dim / 2, slots = half / P, runs = a.runs, run = a.run_heads;
   const int64_t total = a.n * runs * slots;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
@@ -135,7 +161,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     const uint32_t h1 = min(h0 + run, static_cast<uint32_t>(a.heads));
     const T* x = static_cast<const T*>(a.x) + r * a.x_row + slot * E;
     T* y = static_cast<T*>(a.y) + r * a.y_row + slot * E;
-    Part<T, E> lo[kUnroll], hi[HALVES ? kUnroll : 1];
+    Part<T, E, WHOLE> lo[kUnroll], hi[HALVES ? kUnroll : 1];
     const auto load = [&](uint32_t h) {
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u)
@@ -171,7 +197,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
   }
 }
 
-template <typename T, int P, bool HALVES>
+template <typename T, int P, bool HALVES, bool WHOLE>
 cudaError_t launch(RotaryArgs a, int num_sms, cudaStream_t stream) {
   // As many heads in one run as leave every SM its threads (2,048): fewer angles to
   // compute, but a short call is spread over the device.
@@ -184,17 +210,24 @@ cudaError_t launch(RotaryArgs a, int num_sms, cudaStream_t stream) {
   const int64_t total = a.n * a.runs * slots;
   const int64_t blocks = std::min((total + kThreads - 1) / kThreads,
                                   static_cast<int64_t>(num_sms) * 64);
-  return launch_pdl(rotary_kernel<T, P, HALVES>, dim3(static_cast<unsigned>(blocks)),
+  return launch_pdl(rotary_kernel<T, P, HALVES, WHOLE>, dim3(static_cast<unsigned>(blocks)),
                     dim3(kThreads), a.pairs * sizeof(double), stream, a);
 }
 
-template <typename T, int WIDE>  // WIDE: elements of 16 bytes
-cudaError_t pick(const RotaryArgs& a, bool vector, int num_sms, cudaStream_t stream) {
-  if (a.halves)
-    return vector && a.head_dim / 2 % WIDE == 0 ? launch<T, WIDE, true>(a, num_sms, stream)
-                                                : launch<T, 1, true>(a, num_sms, stream);
-  return vector && a.head_dim % WIDE == 0 ? launch<T, WIDE / 2, false>(a, num_sms, stream)
-                                          : launch<T, 1, false>(a, num_sms, stream);
+// The widest access that every part of a head vector is a multiple of.
+template <typename T>
+cudaError_t pick(const RotaryArgs& a, int align, int num_sms, cudaStream_t stream) {
+  constexpr int kEsz = static_cast<int>(sizeof(T));
+  if (a.halves) {
+    if (align == 16) return launch<T, 16 / kEsz, true, true>(a, num_sms, stream);
+    if (align == 8) return launch<T, 8 / kEsz, true, true>(a, num_sms, stream);
+    if (align == 4) return launch<T, 4 / kEsz, true, true>(a, num_sms, stream);
+    return launch<T, 1, true, true>(a, num_sms, stream);
+  }
+  if (align == 16) return launch<T, 8 / kEsz, false, true>(a, num_sms, stream);
+  if (align == 8) return launch<T, 4 / kEsz, false, true>(a, num_sms, stream);
+  if (align == 2 * kEsz) return launch<T, 1, false, true>(a, num_sms, stream);
+  return launch<T, 1, false, false>(a, num_sms, stream);  // pairs across a border
 }
 
 }  // namespace
@@ -202,11 +235,12 @@ cudaError_t pick(const RotaryArgs& a, bool vector, int num_sms, cudaStream_t str
 cudaError_t launch_rotary(const RotaryArgs& a, int num_sms, cudaStream_t stream) {
   const int64_t esz = a.bf16 ? 2 : 4;
   uintptr_t bits = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y);
+  bits |= static_cast<uintptr_t>(a.head_dim / (a.halves ? 2 : 1) * esz);
   if (a.n > 1) bits |= static_cast<uintptr_t>((a.x_row | a.y_row) * esz);
   if (a.heads > 1) bits |= static_cast<uintptr_t>((a.x_head | a.y_head) * esz);
-  const bool vector = bits % 16 == 0;
-  return a.bf16 ? pick<__nv_bfloat16, 8>(a, vector, num_sms, stream)
-                : pick<float, 4>(a, vector, num_sms, stream);
+  const int align = static_cast<int>(std::min<uintptr_t>(bits & (~bits + 1), 16));
+  return a.bf16 ? pick<__nv_bfloat16>(a, align, num_sms, stream)
+                : pick<float>(a, align, num_sms, stream);
 }
 
 }  // namespace subm3d
