@@ -868,14 +868,29 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       if (!ax.on[k]) continue;
+      float* at = mine + k * t.step * E;
+      if constexpr (E % 4 == 0) {  // 16 bytes: single words would meet in an eighth of the banks
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const int e = k * E + i, c = k * t.step * E + i;
-        float lo, hi;
-        f2_unpack(dw[e / 2], lo, hi);
-        mine[c] = e % 2 ? hi : lo;
-        f2_unpack(db[e / 2], lo, hi);
-        mine[a.c + c] = e % 2 ? hi : lo;
+        for (int i = 0; i < E; i += 4) {
+          const int j = (k * E + i) / 2;
+          float4 f;
+          f2_unpack(dw[j], f.x, f.y);
+          f2_unpack(dw[j + 1], f.z, f.w);
+          *reinterpret_cast<float4*>(at + i) = f;
+          f2_unpack(db[j], f.x, f.y);
+          f2_unpack(db[j + 1], f.z, f.w);
+          *reinterpret_cast<float4*>(at + a.c + i) = f;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          const int e = k * E + i;
+          float lo, hi;
+          f2_unpack(dw[e / 2], lo, hi);
+          at[i] = e % 2 ? hi : lo;
+          f2_unpack(db[e / 2], lo, hi);
+          at[a.c + i] = e % 2 ? hi : lo;
+        }
       }
     }
   }

@@ -114,6 +114,27 @@ def test_layouts_of_memory(S, d):
         assert torch.equal(S.rotary(x[:, 0], pos), want[:, 0])
 
 
+@pytest.mark.parametrize("d", [64, 72, 68, 70])
+@pytest.mark.parametrize("start", [0, 1, 2, 4, 8])
+def test_every_alignment(S, d, start):
+    """Vectors that start on 2, 4, 8 or 16 bytes, in x, in the output or in both: the bits of
+    aligned ones, and nothing beside them is written."""
+    for dtype in (BF, F32):
+        for interleaved in (True, False):
+            x, pos = _case(61, 9, d, dtype, 3, 100, d)
+            want = S.rotary(x, pos, interleaved=interleaved)
+            size = 61 * 9 * d
+            src = torch.full((size + 16,), float("nan"), device="cuda", dtype=dtype)
+            dst = torch.full((size + 16,), 5.0, device="cuda", dtype=dtype)
+            xs, ys = (b[start:start + size].view(61, 9, d) for b in (src, dst))
+            xs.copy_(x)
+            S.rotary(x, pos, interleaved=interleaved, out=ys)
+            assert torch.equal(ys, want) and (dst[:start] == 5).all() and (dst[start + size:] == 5).all()
+            assert torch.equal(S.rotary(xs, pos, interleaved=interleaved), want)
+            S.rotary(xs, pos, interleaved=interleaved, out=xs)
+            assert torch.equal(xs, want)
+
+
 def test_round_trip_and_empty(S):
     x, pos = _case(500, 3, 60, F32, 3, 10 ** 6, 3)
     back = S.rotary(S.rotary(x, pos), pos, inverse=True)
