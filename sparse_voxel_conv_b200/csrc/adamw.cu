@@ -20,7 +20,7 @@
 // Bound by HBM: 28 bytes an element with fp32 weights and 32-bit moments (28.3 M
 // elements 119 us, 6.65 TB/s, the copy rate), 18.1 with bf16 weights, fp32 gradients
 // and masters and 8-bit moments (56.6 M elements 158 us at full clock, 6.5 TB/s; 172
-// in a sustained run, whose power lowers the clock: its 69 instructions an element
+// in a sustained run, whose power lowers the clock: its 67 instructions an element
 // count).  A thread takes 8 consecutive elements: 16-byte accesses, and a block of 32
 // elements is four lanes', whose largest magnitude two shuffles find.  Arithmetic on
 // pairs (f32x2).  Four blocks of 256 threads an SM: with five or six the registers

@@ -288,7 +288,7 @@ constexpr int kFewestLanes = 4;   // of a team: 16 bytes of 64 channels a lane a
 // elements of a row without spilling (single-element loads hold half as many), the
 // gradient 128 registers.  A forward block has up to kRowBlock threads, or one wider
 // team; the gradient's blocks fill an SM each, so that few partial sums are left to
-// join (16,384 x 1,536 bf16: 35.7 us, 40.3 with two blocks an SM and a slower join).
+// join (16,384 x 1,536 bf16: 33.4 us; 40.3 with two blocks an SM and a slower join).
 constexpr int row_registers(int e) { return e > 1 ? 80 : 64; }
 constexpr int row_threads(int e) { return e > 1 ? 768 : 1024; }
 constexpr int kRowBlock = 256, kGradThreads = 512;
