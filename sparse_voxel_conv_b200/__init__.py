@@ -4,8 +4,9 @@ The compute path lives in libsubm3d.so (C ABI in include/subm3d.h): a GPU
 hash-table neighbour-map build and an implicit gather-GEMM forward on sm_100a
 tcgen05 tensor cores (bf16, fp32 accumulation in TMEM), plus an fp32
 CUDA-core path; and what stands around it in a trained block: layer norm with
-its gradients, rotary positions from voxel coordinates, AdamW.  This package is the thin Python layer over it.  Importing
-it loads the library and fails loudly if it is not built.
+its gradients, rotary positions from voxel coordinates, AdamW.  This package is
+the thin Python layer over it.  Importing it loads the library and fails loudly
+if it is not built.
 """
 from . import _abi
 from ._abi import Subm3dError

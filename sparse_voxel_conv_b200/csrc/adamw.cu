@@ -47,7 +47,9 @@ __device__ __forceinline__ f2 f2_set(float v) { return f2_pack(v, v); }
 // A product that keeps its own rounding.  (The assembler joins a mul.f32x2 with the
 // add.f32x2 behind it into one fma in spite of their .rn; it cannot join an fma whose
 // addend, -0, it does not know: a parameter of the kernel.)
-__device__ __forceinline__ f2 product(f2 a, f2 b, f2 minus_zero) { return f2_fma(a, b, minus_zero); }
+__device__ __forceinline__ f2 product(f2 a, f2 b, f2 minus_zero) {
+  return f2_fma(a, b, minus_zero);
+}
 
 constexpr int kThreads = 256;
 constexpr int kEach = 8;                           // consecutive elements of a thread
@@ -73,7 +75,8 @@ __device__ __forceinline__ Hyper hyper_of(const AdamWStep& a) {
   int64_t t = a.step;
   if (a.step_device || a.lr_device) {
     if (a.step_device) t = *static_cast<const volatile int32_t*>(a.step_device);
-    const double lr = a.lr_device ? static_cast<double>(*static_cast<const volatile float*>(a.lr_device)) : a.lr;
+    double lr = a.lr;
+    if (a.lr_device) lr = *static_cast<const volatile float*>(a.lr_device);
     const double td = static_cast<double>(t);
     h.step_size = static_cast<float>(lr / -expm1(td * a.log_beta1));
     h.inv_sqrt_bc2 = static_cast<float>(rsqrt(-expm1(td * a.log_beta2)));
@@ -135,7 +138,8 @@ __device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c
 template <bool WHOLE>
 __device__ __forceinline__ void load(f2 (&v)[kPairs], const float* p, int count) {
   if constexpr (WHOLE) {
-    const float4 lo = reinterpret_cast<const float4*>(p)[0], hi = reinterpret_cast<const float4*>(p)[1];
+    const float4 lo = reinterpret_cast<const float4*>(p)[0];
+    const float4 hi = reinterpret_cast<const float4*>(p)[1];
     v[0] = f2_pack(lo.x, lo.y), v[1] = f2_pack(lo.z, lo.w);
     v[2] = f2_pack(hi.x, hi.y), v[3] = f2_pack(hi.z, hi.w);
   } else {
@@ -297,7 +301,9 @@ __device__ __forceinline__ void step_elements(const AdamWStep& a, const Hyper& h
     f2_unpack(v[j], lo, hi);
     if (BITS8) {
       root[j] = root_pair(v[j]);
-      outside |= max(__float_as_uint(lo) - kRootFirst, __float_as_uint(hi) - kRootFirst) >= kRootCount;
+      const uint32_t from0 = __float_as_uint(lo) - kRootFirst;
+      const uint32_t from1 = __float_as_uint(hi) - kRootFirst;
+      outside |= max(from0, from1) >= kRootCount;
     } else {
       root[j] = f2_pack(root_fast(lo), root_fast(hi));
     }

@@ -520,7 +520,9 @@ struct Ahead {
     }
   }
 };
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
 template <int PENDING>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
@@ -605,8 +607,10 @@ __device__ __forceinline__ void load_affine(f2 (&w)[V * E / 2], const void* p, b
       const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + c);
       const uint32_t words[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-      for (int i = 0; i < E; ++i)
-        v[k * E + i] = __uint_as_float(i % 2 ? words[i / 2 % 4] & 0xFFFF0000u : words[i / 2 % 4] << 16);
+      for (int i = 0; i < E; ++i) {
+        const uint32_t word = words[i / 2 % 4];
+        v[k * E + i] = __uint_as_float(i % 2 ? word & 0xFFFF0000u : word << 16);
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < E; ++i) v[k * E + i] = affine_at(p, bf16, c + i);
@@ -950,7 +954,8 @@ RowPlan row_plan(int32_t c, bool bf16, int align) {
 int block_threads(int lanes, int64_t n, int most, int num_sms) {
   const int unit = std::max(lanes, 32);
   int threads = std::max(most / unit, 1) * unit;
-  while (threads >= 2 * unit && threads > 128 && threads / lanes * static_cast<int64_t>(num_sms) > n)
+  while (threads >= 2 * unit && threads > 128 &&
+         threads / lanes * static_cast<int64_t>(num_sms) > n)
     threads = threads / 2 / unit * unit;
   return threads;
 }
@@ -1043,7 +1048,8 @@ cudaError_t launch_layer_norm(const LayerNormArgs& in, int num_sms, cudaStream_t
   const RowPlan p = row_plan(a.c, a.bf16, align);
   const int64_t row_bytes = a.x_stride * (a.bf16 ? 2 : 4);
   a.row_bytes = static_cast<uint32_t>(row_bytes);
-  if (p.lanes > 0 && a.n <= kMaxRows && row_bytes <= 0xFFFFFFFFll) return SUBM3D_ROW_PLAN(launch_norm_rows, a, p, a, p, num_sms, stream);
+  if (p.lanes > 0 && a.n <= kMaxRows && row_bytes <= 0xFFFFFFFFll)
+    return SUBM3D_ROW_PLAN(launch_norm_rows, a, p, a, p, num_sms, stream);
   const dim3 grid(static_cast<unsigned>(std::min(a.n, static_cast<int64_t>(num_sms) * 8)));
   return a.bf16 ? launch_pdl(norm_any_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, stream, a)
                 : launch_pdl(norm_any_kernel<float>, grid, dim3(kThreads), 0, stream, a);
@@ -1060,7 +1066,8 @@ cudaError_t launch_layer_norm_grad(const LayerNormGradArgs& in, int num_sms, cud
   const int64_t x_bytes = a.x_stride * (a.bf16 ? 2 : 4), dy_bytes = a.dy_stride * (a.bf16 ? 2 : 4);
   a.x_row_bytes = static_cast<uint32_t>(x_bytes);
   a.dy_row_bytes = static_cast<uint32_t>(dy_bytes);
-  if (p.lanes > 0 && a.n <= kMaxRows && std::max(x_bytes, dy_bytes) <= 0xFFFFFFFFll) return SUBM3D_ROW_PLAN(launch_grad_rows, a, p, a, p, num_sms, stream);
+  if (p.lanes > 0 && a.n <= kMaxRows && std::max(x_bytes, dy_bytes) <= 0xFFFFFFFFll)
+    return SUBM3D_ROW_PLAN(launch_grad_rows, a, p, a, p, num_sms, stream);
   if (a.dx) {
     const int64_t blocks = std::min(a.n, static_cast<int64_t>(num_sms) * 8);
     const dim3 grid(static_cast<unsigned>(blocks));

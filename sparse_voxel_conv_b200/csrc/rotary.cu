@@ -17,8 +17,8 @@
 // 6.6 TB/s).  A thread takes the P pairs of one load, as wide as the head vectors'
 // alignment allows up to 16 bytes (two loads half a vector apart in the halves
 // layout), computes their cos and sin once, while its first loads are on their way,
-// and keeps them in registers over a run of the row's heads.  With a head or two a row the angles bound it instead (131,072 x 1
-// x 64 bf16: 21 us).
+// and keeps them in registers over a run of the row's heads.  With a head or two a
+// row the angles bound it instead (131,072 x 1 x 64 bf16: 21 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -100,9 +100,11 @@ __device__ __forceinline__ void cos_sin(const RotaryArgs& a, const double* turns
 #pragma unroll
   for (int i = 0; i < kRotaryMaxAxes; ++i) {
     pos[i] = 0.0;
-    if (i < a.axes)
-      pos[i] = a.pos_f32 ? static_cast<double>(static_cast<const float*>(a.pos)[r * a.pos_stride + i])
-                         : static_cast<double>(static_cast<const int32_t*>(a.pos)[r * a.pos_stride + i]);
+    if (i < a.axes) {
+      const int64_t at = r * a.pos_stride + i;
+      pos[i] = a.pos_f32 ? static_cast<double>(static_cast<const float*>(a.pos)[at])
+                         : static_cast<double>(static_cast<const int32_t*>(a.pos)[at]);
+    }
   }
   const int e0 = a.axis_pairs[0], e1 = e0 + a.axis_pairs[1], e2 = e1 + a.axis_pairs[2];
 #pragma unroll

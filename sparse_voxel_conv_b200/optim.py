@@ -119,7 +119,8 @@ class AdamW(torch.optim.Optimizer):
     state_bits: 32, or 8 for moments in about a byte each (see adamw_step).
     master_weights: keep float32 masters of bfloat16 parameters in the state;
     without them a bfloat16 weight loses every change below half its spacing.
-    seed: of the 8-bit rounding.  Parameters must be contiguous CUDA tensors.  In a captured graph call adamw_step() with a device step instead.
+    seed: of the 8-bit rounding.  Parameters must be contiguous CUDA tensors.  In a
+    captured graph call adamw_step() with a device step instead.
     """
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
