@@ -134,6 +134,49 @@ def test_strided_rows(S, c, dtype):
     assert torch.isfinite(y0).all() and all(torch.isfinite(t).all() for t in g0)
 
 
+@pytest.mark.parametrize("n,c", [(60_001, 7), (60_001, 65), (30_005, 75), (30_003, 203), (20_002, 250), (20_009, 505),
+                                 (20_001, 509), (9_001, 1001), (9_006, 1018), (5_003, 1030), (3_001, 2047), (2_999, 2049),
+                                 (1_501, 4095), (1_203, 4097)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rows_between_borders(S, n, c, dtype):
+    """Widths that are no multiple of 16 bytes, with more rows than there are teams, so that
+    each team has several: contiguous, in a wider matrix whose rows lie alike against the
+    borders, and in one whose rows do not."""
+    act = [None, "gelu", "silu"][n % 3]
+    x, dy, w, b = _make(n, c, dtype, "fp32", c)
+    _both(S, x, dy, w, b, 1e-5, act, f"[{n}, {c}] {dtype} {act}")
+    ref = R.Norm(x, w, b, 1e-5, act)
+    want, bound = ref.backward(dy)
+    for pad in (8, 3):
+        wide_x = torch.full((n, c + pad), float("nan"), dtype=dtype, device="cuda")
+        wide_y = wide_x.clone()
+        xs, ds = wide_x[:, :c], wide_y[:, :c]
+        xs.copy_(x)
+        ds.copy_(dy)
+        y, mean, rstd = S.layer_norm_forward(xs, w, b, act=act)
+        R.check(y, ref.y, ref.y_bound(), f"{pad} y")
+        for p, q, e in zip(S.layer_norm_backward(ds, xs, mean, rstd, w, b, act=act), want, bound):
+            R.check(p, q, e, f"{pad} gradient")
+        for p, q, e in zip(S.layer_norm_backward(dy, xs, mean, rstd, w, b, act=act), want, bound):
+            R.check(p, q, e, f"{pad} gradient, dy contiguous")
+
+
+def test_rows_do_not_meet_between_borders(S):
+    """A row of NaN shares its 16-byte parts with its neighbours and not its values."""
+    for dtype in (BF, F32):
+        for c in (7, 65, 203, 1001):
+            x, dy, w, b = _make(20_000, c, dtype, "fp32", 16)
+            y0, m0, r0 = S.layer_norm_forward(x, w, b, act="silu")
+            d0 = S.layer_norm_backward(dy, x, m0, r0, w, b, act="silu")[0]
+            bad, bad_dy = x.clone(), dy.clone()
+            bad[::7], bad_dy[::7] = float("nan"), float("inf")
+            y, mean, rstd = S.layer_norm_forward(bad, w, b, act="silu")
+            dx = S.layer_norm_backward(bad_dy, bad, mean, rstd, w, b, act="silu")[0]
+            keep = torch.arange(20_000, device="cuda") % 7 != 0
+            assert torch.equal(y[keep], y0[keep]) and torch.equal(dx[keep], d0[keep])
+            assert torch.isnan(y[::7]).all() and torch.isnan(dx[::7]).all()
+
+
 def test_rows_do_not_meet(S):
     """A row with a NaN or an infinity spoils itself (and the column sums), no other row."""
     for c in (64, 77, 1536):
