@@ -278,3 +278,35 @@ def test_gradients_that_are_not_contiguous(S):
     S.AdamW([a]).step()
     S.AdamW([b]).step()
     assert torch.equal(a, b)
+
+
+def test_another_current_device(S, monkeypatch):
+    """Tensors of a device that is not the current one: the call is made again with theirs
+    current (here told by a first answer that names another one)."""
+    import sparse_voxel_conv_b200.norm as norm
+    import sparse_voxel_conv_b200.optim as optim
+    import sparse_voxel_conv_b200.positions as positions
+
+    x, dy = torch.randn(50, 64, device="cuda"), torch.randn(50, 64, device="cuda")
+    w, b = torch.rand(64, device="cuda"), torch.rand(64, device="cuda")
+    pos = torch.randint(0, 9, (50, 3), device="cuda", dtype=torch.int32)
+
+    def calls():
+        y, mean, rstd = S.layer_norm_forward(x, w, b, act="silu")
+        out = [y, *S.layer_norm_backward(dy, x, mean, rstd, w, b, act="silu"), S.layer_norm(x, w, b), S.rotary(x, pos)]
+        p, g, m, v = (torch.ones(40, device="cuda") for _ in range(4))
+        S.adamw_step([p], [g], [m], [v], 2)
+        return out + [p, m, v]
+
+    want = calls()
+    asked = []
+    for module in (norm, optim, positions):
+        real = module._current_device
+
+        def first_another(real=real):
+            asked.append(None)
+            return 99 if len(asked) % 2 else real()
+
+        monkeypatch.setattr(module, "_current_device", first_another)
+    got = calls()
+    assert len(asked) == 10 and all(torch.equal(p, q) for p, q in zip(got, want))
