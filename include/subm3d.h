@@ -407,7 +407,7 @@ SUBM3D_API subm3d_status subm3d_pool(const subm3d_map* fine, const int32_t* coor
  *   mean = sum x / C,  rstd = 1 / sqrt(sum (x - mean)^2 / C + eps)
  *
  * (the LayerNorm -> activation that stands before a residual block's
- * convolution; the pages' "gk32_lnormrow" with an activation).  fp32 arithmetic,
+ * convolution; the pages' layer norm, with an activation).  fp32 arithmetic,
  * y rounded once.
  *
  *   x         (device) [N, C] in dtype, rows x_stride elements apart (>= C).
@@ -454,8 +454,8 @@ SUBM3D_API subm3d_status subm3d_layer_norm_backward(
 
 /*
  * Rotary positions with 1 to 4 axes: for voxels, the axes z, y, x of their
- * coordinates (the pages' rope_phases_from_coords; trellis_sparse_mrp_mlx commit
- * log: 63 frequencies padded to 64 with 1 + 0j).
+ * coordinates (trellis_sparse_mrp_mlx commit log: phases from the sparse
+ * coordinates, 63 frequencies padded to 64 with 1 + 0j).
  *
  * A head vector of head_dim channels is head_dim / 2 pairs.  The first
  * axis_pairs[0] of them turn with axis 0 of the row's position, the next

@@ -1,9 +1,9 @@
 """Layer norm over a voxel's channels, with an activation applied on the way.
 
 The norm -> activation that stands before the convolutions of a residual block
-(the pages' LayerNorm kernel "gk32_lnormrow", lingbot-map README; here with the
-activation fused), its backward pass with the reduction of the weight's
-gradient, and a module over SparseTensor.  All of it runs in libsubm3d.so.
+(the lingbot-map README lists a layer norm; here the activation is fused into it),
+its backward pass with the reduction of the weight's gradient, and a module over
+SparseTensor.  All of it runs in libsubm3d.so.
 """
 from __future__ import annotations
 

@@ -1,9 +1,8 @@
 """Rotary positions from voxel coordinates (or any positions with 1 to 4 axes).
 
 The pages' flow models turn queries and keys by phases made from the sparse
-coordinates (rope_phases_from_coords, trellis_sparse_mrp_mlx commit log): each of
-the axes z, y, x has its share of a head's channel pairs, and pairs that are left
-over keep their values.  It runs in libsubm3d.so.
+coordinates (trellis_sparse_mrp_mlx commit log): each of the axes z, y, x has its
+share of a head's channel pairs, and pairs that are left over keep their values.  It runs in libsubm3d.so.
 """
 from __future__ import annotations
 
