@@ -277,6 +277,7 @@ struct LayerNormGradArgs {
   int64_t n = 0, x_stride = 0, dy_stride = 0;
   int32_t c = 0, act = 0;
   uint32_t x_row_bytes = 0, dy_row_bytes = 0;  // the strides in bytes (set by the launch)
+  uint32_t zero = 0;
   bool bf16 = false, affine_bf16 = false;
 };
 int64_t layer_norm_chunks(int64_t n, int32_t channels);

@@ -722,6 +722,89 @@ __global__ void __maxnreg__(row_registers(E)) norm_row_kernel(LayerNormArgs a, i
   if constexpr (A::kAsync) copies_wait<0>();
 }
 
+// The block's column sums of dw and db into partial[block][2][C] (or straight into dweight
+// and dbias, for a grid of one); all threads of the block, done with the rows' slots.
+template <typename T, int E, int V, int LANES>
+__device__ __forceinline__ void leave_sums(const LayerNormGradArgs& a, const Team& t,
+                                           const bool (&on)[V], f2 (&dw)[V * E / 2],
+                                           f2 (&db)[V * E / 2], uint8_t* ring) {
+  constexpr bool WIDE = LANES == 0;
+  constexpr int N = V * E;
+  // The lanes with the same columns: first the teams of a warp by shuffles, then the
+  // block's warps (or wider teams) through shared memory, where the rows' slots hold
+  // their sums now, [groups][2][C].
+  if (!WIDE) {
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2)
+      if (o >= LANES) {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+          dw[i] = f2_add(dw[i], __shfl_xor_sync(0xFFFFFFFFu, dw[i], o));
+          db[i] = f2_add(db[i], __shfl_xor_sync(0xFFFFFFFFu, db[i], o));
+        }
+      }
+  }
+  __syncthreads();
+  float* sums = reinterpret_cast<float*>(ring);
+  const int groups = WIDE ? blockDim.x / t.lanes : blockDim.x / 32;
+  if (t.sub == 0) {
+    float* mine = sums + (WIDE ? t.id : static_cast<int>(threadIdx.x) / 32) * 2 * a.c +
+                  t.first * E;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      if (!on[k]) continue;
+      float* at = mine + k * t.step * E;
+      if constexpr (E % 4 == 0) {  // 16 bytes: single words would meet in an eighth of the banks
+#pragma unroll
+        for (int i = 0; i < E; i += 4) {
+          const int j = (k * E + i) / 2;
+          float4 f;
+          f2_unpack(dw[j], f.x, f.y);
+          f2_unpack(dw[j + 1], f.z, f.w);
+          *reinterpret_cast<float4*>(at + i) = f;
+          f2_unpack(db[j], f.x, f.y);
+          f2_unpack(db[j + 1], f.z, f.w);
+          *reinterpret_cast<float4*>(at + a.c + i) = f;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          const int e = k * E + i;
+          float lo, hi;
+          f2_unpack(dw[e / 2], lo, hi);
+          at[i] = e % 2 ? hi : lo;
+          f2_unpack(db[e / 2], lo, hi);
+          at[a.c + i] = e % 2 ? hi : lo;
+        }
+      }
+    }
+  }
+  __syncthreads();
+  const int group = 2 * a.c, step = blockDim.x;
+  // the groups' sums of `count` columns from `first` on, four columns under way
+  const auto add_up = [&](float* out, int first, int count) {
+    const float* from = sums + first;
+    for (int c = threadIdx.x; c < count; c += 4 * step) {
+      float sum[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum[j] = c + j * step < count ? from[c + j * step] : 0.0f;
+      for (int k = 1; k < groups; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (c + j * step < count) sum[j] += from[k * group + c + j * step];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c + j * step < count) out[c + j * step] = sum[j];
+    }
+  };
+  if (gridDim.x > 1) {
+    add_up(a.partial + static_cast<int64_t>(blockIdx.x) * group, 0, group);
+  } else {
+    if (a.dweight) add_up(a.dweight, 0, a.c);
+    if (a.dbias) add_up(a.dbias, a.c, a.c);
+  }
+}
+
 // Shared memory of a warp of the gradient kernel.
 template <typename T, int E, int V, int ACT>
 __host__ __device__ constexpr uint32_t grad_warp_bytes() {
@@ -729,8 +812,7 @@ __host__ __device__ constexpr uint32_t grad_warp_bytes() {
   return 2 * Ahead<T, E, V, S>::kWarp + S * 256 + (ACT != kActNone ? V * E * 128 : 0);
 }
 
-// dx of the team's rows, and the block's column sums of dz xhat and dz into
-// partial[block][2][C] (or straight into dweight and dbias, for a grid of one).
+// dx of the team's rows, and the block's column sums of dz xhat and dz.
 template <typename T, int E, int V, int ACT, int LANES>
 __global__ void __launch_bounds__(kGradThreads, 1)
     norm_grad_row_kernel(LayerNormGradArgs a, int team_lanes) {
@@ -849,79 +931,134 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   }
   copies_wait<0>();  // also those behind the last row: the slots are free now
   if (!a.partial) return;
-  // The lanes with the same columns: first the teams of a warp by shuffles, then the
-  // block's warps (or wider teams) through shared memory, where the rows' slots hold
-  // their sums now, [groups][2][C].
-  if (!WIDE) {
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2)
-      if (o >= lanes) {
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-          dw[i] = f2_add(dw[i], __shfl_xor_sync(0xFFFFFFFFu, dw[i], o));
-          db[i] = f2_add(db[i], __shfl_xor_sync(0xFFFFFFFFu, db[i], o));
-        }
-      }
-  }
-  __syncthreads();
-  float* sums = reinterpret_cast<float*>(ring);
-  const int groups = WIDE ? blockDim.x / lanes : blockDim.x / 32;
-  if (t.sub == 0) {
-    float* mine = sums + (WIDE ? t.id : static_cast<int>(threadIdx.x) / 32) * 2 * a.c +
-                  t.first * E;
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      if (!ax.on[k]) continue;
-      float* at = mine + k * t.step * E;
-      if constexpr (E % 4 == 0) {  // 16 bytes: single words would meet in an eighth of the banks
-#pragma unroll
-        for (int i = 0; i < E; i += 4) {
-          const int j = (k * E + i) / 2;
-          float4 f;
-          f2_unpack(dw[j], f.x, f.y);
-          f2_unpack(dw[j + 1], f.z, f.w);
-          *reinterpret_cast<float4*>(at + i) = f;
-          f2_unpack(db[j], f.x, f.y);
-          f2_unpack(db[j + 1], f.z, f.w);
-          *reinterpret_cast<float4*>(at + a.c + i) = f;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const int e = k * E + i;
-          float lo, hi;
-          f2_unpack(dw[e / 2], lo, hi);
-          at[i] = e % 2 ? hi : lo;
-          f2_unpack(db[e / 2], lo, hi);
-          at[a.c + i] = e % 2 ? hi : lo;
-        }
-      }
-    }
-  }
-  __syncthreads();
-  const int group = 2 * a.c, step = blockDim.x;
-  // the groups' sums of `count` columns from `first` on, four columns under way
-  const auto add_up = [&](float* out, int first, int count) {
-    const float* from = sums + first;
-    for (int c = threadIdx.x; c < count; c += 4 * step) {
-      float sum[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sum[j] = c + j * step < count ? from[c + j * step] : 0.0f;
-      for (int k = 1; k < groups; ++k)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (c + j * step < count) sum[j] += from[k * group + c + j * step];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (c + j * step < count) out[c + j * step] = sum[j];
+  leave_sums<T, E, V, LANES>(a, t, ax.on, dw, db, ring);
+}
+
+// The same for bf16 rows of 32 V x 8 elements at most, V > 2, without an activation: a
+// warp a row.  Only dw and db stay in registers (16 V of them); xhat and g cost a few
+// instructions a pair, so they are formed again from the row's slots for dx, and the
+// weights lie in shared memory.  No exchange between warps, and a third fewer
+// instructions than with a row over several warps; but more sums to join in a block,
+// so it takes kLongRows rows a warp to pay (768 channels: 32,768 rows 32.9 us, 39.2 over
+// several warps; 8,192 rows 14.3 and 14.4; 4,096 rows of 1,536 channels 15.2 and 14.2).
+constexpr int long_warps(int v) { return v > 4 ? 12 : 16; }  // that the registers allow
+constexpr int kLongRows = 4;
+template <int V>
+__host__ __device__ constexpr uint32_t long_weight_bytes() {
+  return V * 32 * 8 * 4;
+}
+template <int V>
+__global__ void __launch_bounds__(long_warps(V) * 32, 1)
+    norm_grad_long_kernel(LayerNormGradArgs a) {
+  using T = __nv_bfloat16;
+  constexpr int E = 8, N = V * E;
+  using A = Ahead<T, E, V, 2>;
+  static_assert(A::kAsync && A::kFront == 1, "one row ahead, in the other stage");
+  extern __shared__ __align__(16) uint8_t ring[];  // weights, rows; at the end the sums
+  pdl_wait();
+  const Team t = team_of<V, 32>(32);
+  const int vecs = a.c / E, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const float inv_c = 1.0f / static_cast<float>(a.c);
+  const uint32_t weights = kept(smem_u32(ring) + lane * 16);  // [V][2][32] x 4 floats
+  const uint32_t rows = smem_u32(ring) + long_weight_bytes<V>() + warp * 2 * A::kWarp;
+  A ax, ay;
+  ax.init(rows, a.x, t, vecs);
+  ay.init(rows + A::kWarp, a.dy, t, vecs);
+  const uint32_t n = static_cast<uint32_t>(a.n);
+  float next_mean = 0.0f, next_rstd = 0.0f;
+  const auto fetch = [&](uint32_t at, uint32_t r) {
+    const bool live = r < n;
+    ax.fetch(at, r, a.x_row_bytes, live, t);
+    ay.fetch(at, r, a.dy_row_bytes, live, t);
+    copies_commit();
+    if (live) {
+      next_mean = *static_cast<const volatile float*>(a.mean + r);
+      next_rstd = *static_cast<const volatile float*>(a.rstd + r);
     }
   };
-  if (gridDim.x > 1) {
-    add_up(a.partial + static_cast<int64_t>(blockIdx.x) * group, 0, group);
-  } else {
-    if (a.dweight) add_up(a.dweight, 0, a.c);
-    if (a.dbias) add_up(a.dbias, a.c, a.c);
+  fetch(0, t.row);
+  for (int i = threadIdx.x; i < V * 256; i += blockDim.x) {
+    // float i % 4 of half i / 4 % 2 of the part that lane i / 8 % 32 holds k-th
+    const float w = i < a.c ? (a.weight ? affine_at(a.weight, a.affine_bf16, i) : 1.0f) : 0.0f;
+    const int k = i / 256, of = i / 8 % 32, half = i / 4 % 2;
+    reinterpret_cast<float*>(ring)[((k * 2 + half) * 32 + of) * 4 + i % 4] = w;
   }
+  __syncthreads();
+  f2 dw[N / 2], db[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) dw[i] = db[i] = f2_set(0.0f);
+  T* dx = static_cast<T*>(a.dx) + t.first * E;
+  uint32_t cur = 0;
+  f2 shift, rs;
+  // Zero, by way of the part before: the assembler would load all parts at once, into
+  // more registers than there are.  (a.zero is 0, which it does not know.)
+  uint32_t chain = 0;
+  // xhat, dz and dz w of the k-th part
+  const auto part = [&](int k, f2 (&h)[4], f2 (&z)[4], f2 (&g)[4]) {
+    uint32_t x[4], y[4];
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                 : "r"(ax.mine + cur + chain + k * 512)
+                 : "memory");
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+                 : "r"(ay.mine + cur + chain + k * 512)
+                 : "memory");
+    f2 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; i += 2)
+      asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
+                   : "=l"(w[i]), "=l"(w[i + 1])
+                   : "r"(weights + chain + (k * 2 + i / 2) * 512)
+                   : "memory");
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      h[i] = f2_mul(f2_add(bf16_pair(x[i]), shift), rs);
+      z[i] = bf16_pair(y[i]);
+      g[i] = f2_mul(z[i], w[i]);
+    }
+    chain = (x[0] ^ static_cast<uint32_t>(g[3])) & a.zero;
+  };
+  for (uint32_t r = t.row; r < n; r += t.stride) {
+    copies_wait<0>();
+    shift = f2_set(-next_mean);
+    rs = f2_set(next_rstd);
+    fetch(cur ^ A::kStage, r + t.stride);
+    f2 s0 = f2_set(0.0f), s1 = f2_set(0.0f);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      f2 h[4], z[4], g[4];
+      part(k, h, z, g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        db[k * 4 + i] = f2_add(db[k * 4 + i], z[i]);
+        dw[k * 4 + i] = f2_fma(z[i], h[i], dw[k * 4 + i]);
+        s0 = f2_add(s0, g[i]);
+        s1 = f2_fma(g[i], h[i], s1);
+      }
+    }
+    const float m0 = lanes_sum<32>(f2_sum(s0)), m1 = lanes_sum<32>(f2_sum(s1));
+    if (a.dx) {
+      float rstd, unused;
+      f2_unpack(rs, rstd, unused);
+      const f2 c0 = f2_set(-m0 * inv_c * rstd), c1 = f2_set(-m1 * inv_c * rstd);
+      T* to = dx + static_cast<uint64_t>(r) * static_cast<uint32_t>(a.c);
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        f2 h[4], z[4], g[4];
+        part(k, h, z, g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) g[i] = f2_fma(h[i], c1, f2_fma(g[i], rs, c0));
+        if (ax.on[k])
+          *reinterpret_cast<uint4*>(to + k * 256) = make_uint4(
+              to_bf16_pair(g[0]), to_bf16_pair(g[1]), to_bf16_pair(g[2]), to_bf16_pair(g[3]));
+      }
+    }
+    cur ^= A::kStage;
+  }
+  copies_wait<0>();
+  if (!a.partial) return;
+  leave_sums<T, E, V, 32>(a, t, ax.on, dw, db, ring);
 }
 
 // How a row kernel lies on the rows.
@@ -985,7 +1122,7 @@ cudaError_t allow_smem(size_t bytes) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = uint64_t(1) << (dev & 63);
   if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
-  e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+  e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
   if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_release);
   return e;
 }
@@ -1018,6 +1155,22 @@ cudaError_t launch_grad_rows(const LayerNormGradArgs& a, const RowPlan& p, int n
       blocks_for(p.lanes, threads, a.n, kGradThreads, num_sms, layer_norm_chunks(a.n, a.c));
   e = launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(threads), smem, stream, a,
                  p.lanes);
+  if (e != cudaSuccess || !a.partial || blocks == 1) return e;
+  return launch_join(a, static_cast<int>(blocks), stream);
+}
+
+template <int V>
+cudaError_t launch_grad_long(const LayerNormGradArgs& a, int num_sms, cudaStream_t stream) {
+  const int threads = block_threads(32, a.n, long_warps(V) * 32, num_sms);
+  const size_t rows = 2 * Ahead<__nv_bfloat16, 8, V, 2>::kWarp;
+  const size_t warps = threads / 32;
+  const size_t smem = std::max(long_weight_bytes<V>() + warps * rows, warps * a.c * 8);
+  constexpr auto kernel = norm_grad_long_kernel<V>;
+  cudaError_t e = allow_smem<kernel>(smem);
+  if (e != cudaSuccess) return e;
+  const int64_t blocks =
+      blocks_for(32, threads, a.n, long_warps(V) * 32, num_sms, layer_norm_chunks(a.n, a.c));
+  e = launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(threads), smem, stream, a);
   if (e != cudaSuccess || !a.partial || blocks == 1) return e;
   return launch_join(a, static_cast<int>(blocks), stream);
 }
@@ -1066,7 +1219,14 @@ cudaError_t launch_layer_norm_grad(const LayerNormGradArgs& in, int num_sms, cud
   const int64_t x_bytes = a.x_stride * (a.bf16 ? 2 : 4), dy_bytes = a.dy_stride * (a.bf16 ? 2 : 4);
   a.x_row_bytes = static_cast<uint32_t>(x_bytes);
   a.dy_row_bytes = static_cast<uint32_t>(dy_bytes);
-  if (p.lanes > 0 && a.n <= kMaxRows && std::max(x_bytes, dy_bytes) <= 0xFFFFFFFFll)
+  const bool fits = p.lanes > 0 && a.n <= kMaxRows && std::max(x_bytes, dy_bytes) <= 0xFFFFFFFFll;
+  if (fits && p.lanes > 32 && a.bf16 && p.vec == 8 && a.act == kActNone) {
+    const int v = a.c <= 4 * 256 ? 4 : 6;
+    if (a.c <= v * 256 && a.n >= static_cast<int64_t>(kLongRows) * num_sms * long_warps(v))
+      return v == 4 ? launch_grad_long<4>(a, num_sms, stream)
+                    : launch_grad_long<6>(a, num_sms, stream);
+  }
+  if (fits)
     return SUBM3D_ROW_PLAN(launch_grad_rows, a, p, a, p, num_sms, stream);
   if (a.dx) {
     const int64_t blocks = std::min(a.n, static_cast<int64_t>(num_sms) * 8);

@@ -161,6 +161,31 @@ def test_rows_between_borders(S, n, c, dtype):
             R.check(p, q, e, f"{pad} gradient, dy contiguous")
 
 
+@pytest.mark.parametrize("n,c", [(9_500, 520), (20_001, 768), (9_471, 1024), (9_472, 1024), (9_473, 1000), (7_103, 1032),
+                                 (7_104, 1032), (15_000, 1536), (30_011, 1480), (8_000, 1544)])
+@pytest.mark.parametrize("affine", [None, "fp32", "same"])
+def test_long_rows_without_activation(S, n, c, affine):
+    """Around the change from several warps to one warp a row, in rows and in channels."""
+    x, dy, w, b = _make(n, c, BF, affine, c)
+    _both(S, x, dy, w, b, 1e-5, None, f"[{n}, {c}] {affine}")
+    ref = R.Norm(x, w, b, 1e-5, None)
+    want, bound = ref.backward(dy)
+    wide = torch.full((n, 2 * c + 16), float("nan"), dtype=BF, device="cuda")
+    xs, ds = wide[:, :c], wide[:, c + 8:2 * c + 8]
+    xs.copy_(x)
+    ds.copy_(dy)
+    _, mean, rstd = S.layer_norm_forward(xs, w, b)
+    full = S.layer_norm_backward(ds, xs, mean, rstd, w, b)
+    for p, q, e in zip(full, want, bound):
+        if p is not None:
+            R.check(p, q, e, "strided")
+    only = S.layer_norm_backward(ds, xs, mean, rstd, w, b, wanted=(True, False, False))
+    assert torch.equal(only[0], full[0])
+    rest = S.layer_norm_backward(ds, xs, mean, rstd, w, b, wanted=(False, True, True))
+    for p, q in zip(rest[1:], full[1:]):
+        assert p is None or torch.equal(p, q)
+
+
 def test_rows_do_not_meet_between_borders(S):
     """A row of NaN shares its 16-byte parts with its neighbours and not its values."""
     for dtype in (BF, F32):
