@@ -288,7 +288,8 @@ constexpr int kFewestLanes = 4;   // of a team: 16 bytes of 64 channels a lane a
 // elements of a row without spilling (single-element loads hold half as many), the
 // gradient 128 registers.  A forward block has up to kRowBlock threads, or one wider
 // team; the gradient's blocks fill an SM each, so that few partial sums are left to
-// join (16,384 x 1,536 bf16: 33.4 us; 40.3 with two blocks an SM and a slower join).
+// join (16,384 x 1,536 bf16 over three warps a row: 33.4 us; 40.3 with two blocks an SM
+// and a slower join).
 constexpr int row_registers(int e) { return e > 1 ? 80 : 64; }
 constexpr int row_threads(int e) { return e > 1 ? 768 : 1024; }
 constexpr int kRowBlock = 256, kGradThreads = 512;
@@ -937,10 +938,11 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 // The same for bf16 rows of 32 V x 8 elements at most, V > 2, without an activation: a
 // warp a row.  Only dw and db stay in registers (16 V of them); xhat and g cost a few
 // instructions a pair, so they are formed again from the row's slots for dx, and the
-// weights lie in shared memory.  No exchange between warps, and a third fewer
-// instructions than with a row over several warps; but more sums to join in a block,
-// so it takes kLongRows rows a warp to pay (768 channels: 32,768 rows 32.9 us, 39.2 over
-// several warps; 8,192 rows 14.3 and 14.4; 4,096 rows of 1,536 channels 15.2 and 14.2).
+// weights lie in shared memory.  As many instructions a row as over several warps,
+// but no exchange: warps wait for nobody and hide one another's latency (46 % of the
+// issue slots against 34 %).  A block has more sums to join, so it takes kLongRows rows
+// a warp to pay (768 channels: 32,768 rows 32.9 us, 39.2 over several warps; 8,192 rows
+// 14.3 and 14.4; 4,096 rows of 1,536 channels 15.2 and 14.2).
 constexpr int long_warps(int v) { return v > 4 ? 12 : 16; }  // that the registers allow
 constexpr int kLongRows = 4;
 template <int V>
