@@ -31,11 +31,10 @@ def _rows(t: torch.Tensor, name: str):
 
 
 def _affine(t, name: str, x_dtype, c: int, dev: int):
-    """A weight or bias vector, checked and contiguous (None stays None)."""
-    if t is None:
-        return None
-    if t.dtype is not torch.float32 and t.dtype is not x_dtype:
-        raise ValueError(f"{name} must be float32 or {x_dtype}, got {t.dtype}")
+    """A weight or bias vector, checked and contiguous."""
+    dtype = t.dtype
+    if dtype is not torch.float32 and dtype is not x_dtype:
+        raise ValueError(f"{name} must be float32 or {x_dtype}, got {dtype}")
     if t.dim() != 1 or t.numel() != c:
         raise ValueError(f"{name} must have shape [{c}]")
     if t.get_device() != dev:
@@ -70,11 +69,12 @@ def _norm(x, weight, bias, eps, act, out, stream, stats: bool):
     rows, stride = _rows(x, "x")
     c = rows.shape[-1]
     n = x.numel() // c
-    w = _affine(weight, "weight", x_dtype, c, dev)
-    b = _affine(bias, "bias", x_dtype, c, dev)
+    w = None if weight is None else _affine(weight, "weight", x_dtype, c, dev)
+    b = None if bias is None else _affine(bias, "bias", x_dtype, c, dev)
     affine_dtype = _affine_code(w, b, x_dtype)
     if out is None:
-        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+        y = torch.empty_like(x) if x.is_contiguous() else \
+            torch.empty_like(x, memory_format=torch.contiguous_format)
     else:
         _same_device(dev, "out", out)
         if out.shape != x.shape or out.dtype != x_dtype or not out.is_contiguous():
