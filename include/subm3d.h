@@ -439,8 +439,9 @@ SUBM3D_API subm3d_status subm3d_layer_norm(const void* x, int64_t n, int32_t cha
  *   dweight, dbias  (device) fp32 [C], overwritten; each may be NULL.  The rows
  *             are summed in a fixed order: the same call gives the same bits.
  *   workspace (device) >= subm3d_layer_norm_workspace_bytes(N, C) bytes, 16-byte
- *             aligned, for dweight and dbias (may be NULL when both are).  It
- *             holds nothing between calls.
+ *             aligned, for dweight and dbias (may be NULL when both are, and
+ *             when that is 0 bytes: a small call needs none).  It holds
+ *             nothing between calls.
  *
  * No output may overlap another buffer.  N = 0 writes zeros to dweight and
  * dbias.  Asynchronous.

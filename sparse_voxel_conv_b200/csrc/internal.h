@@ -262,7 +262,7 @@ struct LayerNormArgs {
 cudaError_t launch_layer_norm(const LayerNormArgs& a, int num_sms, cudaStream_t stream);
 
 // Its backward: dx (null: not wanted) in the features' type, dweight and dbias
-// (each may be null) in fp32 through `partial`: fp32 [layer_norm_chunks()][2][C].
+// (each may be null) in fp32 through `partial`: fp32 [layer_norm_chunks()][2][C] (null for one chunk).
 struct LayerNormGradArgs {
   const void* dy = nullptr;
   const void* x = nullptr;
@@ -278,6 +278,7 @@ struct LayerNormGradArgs {
   int32_t c = 0, act = 0;
   uint32_t x_row_bytes = 0, dy_row_bytes = 0;  // the strides in bytes (set by the launch)
   uint32_t zero = 0;
+  bool sums = false;  // dweight or dbias is wanted (set by the launch)
   bool bf16 = false, affine_bf16 = false;
 };
 int64_t layer_norm_chunks(int64_t n, int32_t channels);

@@ -35,8 +35,13 @@ namespace subm3d {
 constexpr int kMaxRowElements = 8192;  // of a row kernel
 
 // The most blocks that leave partial column sums: four on each of 148 SMs.  Fewer for
-// the widest rows, whose sums take the more room the fewer the rows.
+// the widest rows, whose sums take the more room the fewer the rows.  Up to
+// kOneBlock elements (a round of a block's lanes) one block sums them all: no partial
+// sums, no workspace and no second launch, which spares the caller some 4 us.  (4,096
+// elements: 3.6 us by one block, 3.8 by many and their join; 16,384: 6.4 and 3.8.)
+constexpr int64_t kOneBlock = 8192;
 int64_t layer_norm_chunks(int64_t n, int32_t channels) {
+  if (channels <= kMaxRowElements / 2 && n * std::max(channels, 64) <= kOneBlock) return 1;
   return std::min<int64_t>(channels <= kMaxRowElements ? n : (n + 63) / 64, 592);
 }
 
@@ -188,7 +193,8 @@ __global__ void __launch_bounds__(kThreads) norm_dx_any_kernel(LayerNormGradArgs
 }
 
 // Column sums of dz xhat and dz over a chunk of rows: 32 columns a block, 8 rows
-// at a time, into partial[chunk][2][C].
+// at a time, into partial[chunk][2][C] (one chunk:
+// into dweight and dbias).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) norm_dw_any_kernel(LayerNormGradArgs a,
                                                                int64_t rows_per_chunk) {
@@ -216,7 +222,12 @@ __global__ void __launch_bounds__(kThreads) norm_dw_any_kernel(LayerNormGradArgs
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) s += sh[ty][i][lane];
-    a.partial[(static_cast<int64_t>(blockIdx.y) * 2 + ty) * a.c + c] = s;
+    if (gridDim.y > 1) {
+      a.partial[(static_cast<int64_t>(blockIdx.y) * 2 + ty) * a.c + c] = s;
+    } else {
+      float* out = ty == 0 ? a.dweight : a.dbias;
+      if (out) out[c] = s;
+    }
   }
 }
 
@@ -931,7 +942,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                        r < n && a.dx, t);
   }
   copies_wait<0>();  // also those behind the last row: the slots are free now
-  if (!a.partial) return;
+  if (!a.sums) return;
   leave_sums<T, E, V, LANES>(a, t, ax.on, dw, db, ring);
 }
 
@@ -1059,7 +1070,7 @@ __global__ void __launch_bounds__(long_warps(V) * 32, 1)
     cur ^= A::kStage;
   }
   copies_wait<0>();
-  if (!a.partial) return;
+  if (!a.sums) return;
   leave_sums<T, E, V, 32>(a, t, ax.on, dw, db, ring);
 }
 
@@ -1097,6 +1108,13 @@ int block_threads(int lanes, int64_t n, int most, int num_sms) {
          threads / lanes * static_cast<int64_t>(num_sms) > n)
     threads = threads / 2 / unit * unit;
   return threads;
+}
+
+// Of a gradient's only block: a team a row, up to the most.
+int one_block_threads(int lanes, int64_t n) {
+  const int unit = std::max(lanes, 32);
+  const int64_t wanted = (n * lanes + unit - 1) / unit;
+  return static_cast<int>(std::min<int64_t>(wanted, std::max(kGradThreads / unit, 1))) * unit;
 }
 
 // Blocks for n rows: as many as there are teams for, up to what fits on the device
@@ -1146,7 +1164,9 @@ cudaError_t launch_norm_rows(const LayerNormArgs& a, const RowPlan& p, int num_s
 template <typename T, int E, int V, int ACT, int LANES>
 cudaError_t launch_grad_rows(const LayerNormGradArgs& a, const RowPlan& p, int num_sms,
                              cudaStream_t stream) {
-  const int threads = block_threads(p.lanes, a.n, kGradThreads, num_sms);
+  const int threads = layer_norm_chunks(a.n, a.c) > 1
+                          ? block_threads(p.lanes, a.n, kGradThreads, num_sms)
+                          : one_block_threads(p.lanes, a.n);
   const size_t groups = LANES == 0 ? threads / p.lanes : threads / 32;
   const size_t smem =
       std::max<size_t>(threads / 32 * grad_warp_bytes<T, E, V, ACT>(), groups * a.c * 8);
@@ -1157,7 +1177,7 @@ cudaError_t launch_grad_rows(const LayerNormGradArgs& a, const RowPlan& p, int n
       blocks_for(p.lanes, threads, a.n, kGradThreads, num_sms, layer_norm_chunks(a.n, a.c));
   e = launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(threads), smem, stream, a,
                  p.lanes);
-  if (e != cudaSuccess || !a.partial || blocks == 1) return e;
+  if (e != cudaSuccess || !a.sums || blocks == 1) return e;
   return launch_join(a, static_cast<int>(blocks), stream);
 }
 
@@ -1173,7 +1193,7 @@ cudaError_t launch_grad_long(const LayerNormGradArgs& a, int num_sms, cudaStream
   const int64_t blocks =
       blocks_for(32, threads, a.n, long_warps(V) * 32, num_sms, layer_norm_chunks(a.n, a.c));
   e = launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(threads), smem, stream, a);
-  if (e != cudaSuccess || !a.partial || blocks == 1) return e;
+  if (e != cudaSuccess || !a.sums || blocks == 1) return e;
   return launch_join(a, static_cast<int>(blocks), stream);
 }
 
@@ -1213,7 +1233,7 @@ cudaError_t launch_layer_norm(const LayerNormArgs& in, int num_sms, cudaStream_t
 cudaError_t launch_layer_norm_grad(const LayerNormGradArgs& in, int num_sms, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   LayerNormGradArgs a = in;
-  if (!a.dweight && !a.dbias) a.partial = nullptr;
+  a.sums = a.dweight || a.dbias;
   const int align = std::min({rows_align(a.x, a.x_stride, a.bf16),
                               rows_align(a.dy, a.dy_stride, a.bf16),
                               rows_align(a.dx, a.c, a.bf16)});
@@ -1237,7 +1257,7 @@ cudaError_t launch_layer_norm_grad(const LayerNormGradArgs& in, int num_sms, cud
                : launch_pdl(norm_dx_any_kernel<float>, grid, dim3(kThreads), 0, stream, a);
     if (e != cudaSuccess) return e;
   }
-  if (!a.dweight && !a.dbias) return e;
+  if (!a.sums) return e;
   const int64_t chunks = layer_norm_chunks(a.n, a.c);
   const int64_t rows = (a.n + chunks - 1) / chunks;
   const unsigned cols = static_cast<unsigned>((a.c + 31) / 32);
@@ -1245,7 +1265,7 @@ cudaError_t launch_layer_norm_grad(const LayerNormGradArgs& in, int num_sms, cud
   e = a.bf16 ? launch_pdl(norm_dw_any_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, stream, a,
                           rows)
              : launch_pdl(norm_dw_any_kernel<float>, grid, dim3(kThreads), 0, stream, a, rows);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || chunks == 1) return e;
   return launch_join(a, static_cast<int>(chunks), stream);
 }
 

@@ -568,7 +568,8 @@ subm3d_status subm3d_layer_norm(const void* x, int64_t n, int32_t channels, int6
 
 size_t subm3d_layer_norm_workspace_bytes(int64_t n, int32_t channels) {
   if (n < 0 || channels < 1 || channels > kMaxNormChannels) return 0;
-  return static_cast<size_t>(subm3d::layer_norm_chunks(n, channels)) * 2 * channels * 4;
+  const int64_t chunks = subm3d::layer_norm_chunks(n, channels);
+  return chunks > 1 ? static_cast<size_t>(chunks) * 2 * channels * 4 : 0;
 }
 
 subm3d_status subm3d_layer_norm_backward(
@@ -593,10 +594,10 @@ subm3d_status subm3d_layer_norm_backward(
   }
   if (!dx && !dweight && !dbias) return SUBM3D_OK;
   const bool sums = dweight || dbias;
-  if (!dy || !x || !mean || !rstd || (sums && !workspace)) return SUBM3D_E_INVALID;
   const size_t need = sums ? subm3d_layer_norm_workspace_bytes(n, channels) : 0;
+  if (!dy || !x || !mean || !rstd || (need && !workspace)) return SUBM3D_E_INVALID;
   const size_t esz = dtype_bytes(dtype), asz = dtype_bytes(affine_dtype);
-  if (workspace_bytes < need || (sums && !aligned(workspace, 16)) || !aligned(dy, esz) ||
+  if (workspace_bytes < need || (need && !aligned(workspace, 16)) || !aligned(dy, esz) ||
       !aligned(x, esz) || !aligned(dx, esz) || !aligned(weight, asz) || !aligned(bias, asz) ||
       !aligned(mean, 4) || !aligned(rstd, 4))
     return SUBM3D_E_INVALID;
@@ -609,7 +610,7 @@ subm3d_status subm3d_layer_norm_backward(
                   span(dx, rows_bytes(n, channels, channels, esz), true),
                   span(dweight, c4, true),
                   span(dbias, c4, true),
-                  span(sums ? workspace : nullptr, static_cast<int64_t>(need), true)};
+                  span(need ? workspace : nullptr, static_cast<int64_t>(need), true)};
   if (clash(spans, 10)) return SUBM3D_E_INVALID;
   subm3d::LayerNormGradArgs a;
   a.dy = dy;
@@ -621,7 +622,7 @@ subm3d_status subm3d_layer_norm_backward(
   a.dx = dx;
   a.dweight = dweight;
   a.dbias = dbias;
-  a.partial = static_cast<float*>(workspace);
+  a.partial = need ? static_cast<float*>(workspace) : nullptr;
   a.n = n;
   a.x_stride = x_stride;
   a.dy_stride = dy_stride;

@@ -150,7 +150,8 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
     ws_bytes = 0
     if dw is not None or db is not None:
         ws_bytes = _abi.subm3d_layer_norm_workspace_bytes(n, c)
-        ws = mean_c.new_empty(ws_bytes // 4)
+        if ws_bytes:
+            ws = mean_c.new_empty(ws_bytes // 4)
     if stream is not None:
         _on_side_stream(stream, dx, dw, db, ws, _new(xr, x), _new(dr, dy), _new(w, weight),
                         _new(b, bias), _new(mean_c, mean), _new(rstd_c, rstd))

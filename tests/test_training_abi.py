@@ -46,11 +46,13 @@ GRAD = ["dy", "dy_stride", "x", "x_stride", "n", "channels", "dtype", "mean", "r
 
 
 def test_layer_norm_backward(abi):
-    ws = abi.subm3d_layer_norm_workspace_bytes(10, 64)
-    assert ws >= 2 * 64 * 4
+    ws = abi.subm3d_layer_norm_workspace_bytes(100_000, 64)
+    assert ws >= 2 * 2 * 64 * 4
+    assert abi.subm3d_layer_norm_workspace_bytes(10, 64) == 0       # one block needs none
+    assert abi.subm3d_layer_norm_workspace_bytes(100, 1 << 24) >= 2 * 2 * 4 << 24
     assert abi.subm3d_layer_norm_workspace_bytes(-1, 64) == 0 and abi.subm3d_layer_norm_workspace_bytes(10, 0) == 0
     assert abi.subm3d_layer_norm_workspace_bytes(0, 64) == 0
-    ok = dict(dy=at(0), dy_stride=64, x=at(1), x_stride=64, n=10, channels=64, dtype=1, mean=at(2), rstd=at(3),
+    ok = dict(dy=at(0), dy_stride=64, x=at(1), x_stride=64, n=100_000, channels=64, dtype=1, mean=at(2), rstd=at(3),
               weight=at(4), bias=at(5), affine_dtype=0, act=0, dx=at(6), dweight=at(7), dbias=at(8), workspace=at(9),
               workspace_bytes=ws, stream=None)
     f = lambda **o: abi.lib.subm3d_layer_norm_backward(*[{**ok, **o}[k] for k in GRAD])  # noqa: E731
