@@ -35,35 +35,40 @@ def _turn(x, positions, theta, axis_pairs, interleaved, inverse, out, stream):
     pos_f32 = positions.dtype is torch.float32
     if not pos_f32 and positions.dtype is not torch.int32:
         raise ValueError(f"positions must be int32 or float32, got {positions.dtype}")
-    if positions.dim() != 2 or positions.shape[0] != n or not 1 <= positions.shape[1] <= 4:
+    p_shape = positions.shape
+    if len(p_shape) != 2 or p_shape[0] != n or not 1 <= p_shape[1] <= 4:
         raise ValueError(f"positions must have shape [{n}, 1 to 4 axes]")
-    axes = positions.shape[1]
+    axes = p_shape[1]
     if axis_pairs is None:
         axis_pairs = (d // 2 // axes,) * axes
     elif len(axis_pairs) != axes or min(axis_pairs) < 0 or sum(axis_pairs) > d // 2:
         raise ValueError(f"axis_pairs must give each of {axes} axes its pairs, {d // 2} at most")
-    _same_device(dev, "positions", positions)
+    if positions.get_device() != dev:
+        _same_device(dev, "positions", positions)
     x_in, pos_in = x, positions
-    if x.stride(-1) != 1:
+    xs, ps = x.stride(), positions.stride()
+    if xs[-1] != 1:
         if out is x:
             raise ValueError("x must have contiguous channels to be turned in place")
         x = x.contiguous()
-    if positions.stride(1) != 1:
+        xs = x.stride()
+    if ps[1] != 1:
         positions = positions.contiguous()
+        ps = positions.stride()
     if out is None:
-        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+        y = torch.empty_like(x) if x.is_contiguous() else \
+            torch.empty_like(x, memory_format=torch.contiguous_format)
+        ys = (heads * d, d, 1)
     else:
         _same_device(dev, "out", out)
         if out.shape != shape or out.dtype != dtype or out.stride(-1) != 1:
             raise ValueError(f"out must be {dtype} of x's shape with contiguous channels")
-        y = out
+        y, ys = out, out.stride()
     if stream is not None:
         _on_side_stream(stream, _new(x, x_in), _new(positions, pos_in), _new(y, out))
-    xs, ys = x.stride(), y.stride()
     x_head, y_head = (xs[1], ys[1]) if len(shape) == 3 else (0, d)
-    _abi.subm3d_rotary(x, xs[0], x_head, n, heads, d, _DTYPES[dtype], positions, pos_f32,
-                       positions.stride(0), axis_pairs, theta, not interleaved, inverse, y, ys[0],
-                       y_head, stream)
+    _abi.subm3d_rotary(x, xs[0], x_head, n, heads, d, _DTYPES[dtype], positions, pos_f32, ps[0],
+                       axis_pairs, theta, not interleaved, inverse, y, ys[0], y_head, stream)
     if out is not None:
         _written(out)
     return y
