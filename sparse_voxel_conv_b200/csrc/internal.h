@@ -262,7 +262,8 @@ struct LayerNormArgs {
 cudaError_t launch_layer_norm(const LayerNormArgs& a, int num_sms, cudaStream_t stream);
 
 // Its backward: dx (null: not wanted) in the features' type, dweight and dbias
-// (each may be null) in fp32 through `partial`: fp32 [layer_norm_chunks()][2][C] (null for one chunk).
+// (each may be null) in fp32 through `partial`: fp32 [layer_norm_chunks()][2][C] (null for
+// one chunk).
 struct LayerNormGradArgs {
   const void* dy = nullptr;
   const void* x = nullptr;

@@ -193,8 +193,7 @@ __global__ void __launch_bounds__(kThreads) norm_dx_any_kernel(LayerNormGradArgs
 }
 
 // Column sums of dz xhat and dz over a chunk of rows: 32 columns a block, 8 rows
-// at a time, into partial[chunk][2][C] (one chunk:
-// into dweight and dbias).
+// at a time, into partial[chunk][2][C] (one chunk: into dweight and dbias).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) norm_dw_any_kernel(LayerNormGradArgs a,
                                                                int64_t rows_per_chunk) {

@@ -2,7 +2,8 @@
 
 The pages' flow models turn queries and keys by phases made from the sparse
 coordinates (trellis_sparse_mrp_mlx commit log): each of the axes z, y, x has its
-share of a head's channel pairs, and pairs that are left over keep their values.  It runs in libsubm3d.so.
+share of a head's channel pairs, and pairs that are left over keep their values.
+It runs in libsubm3d.so.
 """
 from __future__ import annotations
 
