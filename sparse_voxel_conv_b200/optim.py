@@ -119,8 +119,9 @@ class AdamW(torch.optim.Optimizer):
     state_bits: 32, or 8 for moments in about a byte each (see adamw_step).
     master_weights: keep float32 masters of bfloat16 parameters in the state;
     without them a bfloat16 weight loses every change below half its spacing.
-    seed: of the 8-bit rounding.  Parameters must be contiguous CUDA tensors.  In a
-    captured graph call adamw_step() with a device step instead.
+    seed: of the 8-bit rounding; it is saved and loaded with the groups.  Parameters
+    must be contiguous CUDA tensors.  In a captured graph call adamw_step() with a
+    device step instead.
     """
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
@@ -130,10 +131,26 @@ class AdamW(torch.optim.Optimizer):
             raise ValueError("state_bits must be 32 or 8")
         if lr < 0 or eps < 0 or weight_decay < 0 or not all(0 <= b < 1 for b in betas):
             raise ValueError("lr, eps and weight_decay must not be negative, betas in [0, 1)")
-        self.seed = int(seed)
         super().__init__(params, dict(lr=lr, betas=tuple(betas), eps=eps,
                                       weight_decay=weight_decay, state_bits=state_bits,
-                                      master_weights=master_weights))
+                                      master_weights=master_weights, seed=int(seed)))
+
+    # The seed lies in the parameter groups, which a copy, a file and state_dict() hold: what
+    # is loaded goes on with the saved stream of rounding bits.
+    @property
+    def seed(self) -> int:
+        return self.param_groups[0]["seed"]
+
+    @seed.setter
+    def seed(self, seed: int) -> None:
+        for at in (self.defaults, *self.param_groups):
+            at["seed"] = int(seed)
+
+    def __setstate__(self, state):
+        super().__setstate__(state)
+        for group in self.param_groups:     # saved before the groups held a seed
+            group.setdefault("seed", self.defaults.get("seed", 0))
+        self.defaults["seed"] = self.seed   # of groups that join later
 
     def _state_of(self, p, group):
         st = self.state[p]
@@ -185,7 +202,7 @@ class AdamW(torch.optim.Optimizer):
                            masters=pick("master") if key[3] else None,
                            exp_avg_scales=pick("exp_avg_scale") if bits8 else None,
                            exp_avg_sq_scales=pick("exp_avg_sq_scale") if bits8 else None,
-                           seed=self.seed + 0x632BE5A7 * call)
+                           seed=group["seed"] + 0x632BE5A7 * call)
                 for st in states:
                     st["step"] += 1
                 call += 1

@@ -1,0 +1,63 @@
+"""What the training operators' Python layer decides before any kernel runs.  CPU only."""
+import copy
+import io
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def S():
+    from sparse_voxel_conv_b200 import build
+    build.build()
+    import sparse_voxel_conv_b200 as S
+    return S
+
+
+def _through_file(obj):
+    f = io.BytesIO()
+    torch.save(obj, f)
+    f.seek(0)
+    return torch.load(f, weights_only=False)
+
+
+def _seeds_of(opt, monkeypatch):
+    """The seeds of the calls that one step() makes."""
+    import sparse_voxel_conv_b200.optim as optim
+    seeds = []
+    monkeypatch.setattr(optim, "adamw_step", lambda *a, seed, **k: seeds.append(seed & 0xFFFFFFFF))
+    for group in opt.param_groups:
+        for p in group["params"]:
+            p.grad = torch.ones_like(p)
+    opt.step()
+    return seeds
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_optimizer_keeps_its_seed(S, bits, monkeypatch):
+    """Copied, saved whole, or loaded into an optimizer that was made with another seed, the
+    optimizer goes on with the stream of rounding bits that it had."""
+    make = lambda **k: S.AdamW([dict(params=[torch.nn.Parameter(torch.ones(40))]),  # noqa: E731
+                                dict(params=[torch.nn.Parameter(torch.ones(7))], lr=1e-4)], state_bits=bits, **k)
+    want = [5, 5 + 0x632BE5A7]
+    opt = make(seed=5)
+    assert opt.seed == 5 and _seeds_of(opt, monkeypatch) == want
+    for other in (copy.deepcopy(opt), _through_file(opt)):
+        assert other.seed == 5 and _seeds_of(other, monkeypatch) == want
+        assert other.state[other.param_groups[0]["params"][0]]["step"] == 2
+    resumed = make()
+    assert resumed.seed == 0 and _seeds_of(resumed, monkeypatch) == [0, 0x632BE5A7]
+    resumed.load_state_dict(opt.state_dict())
+    assert resumed.seed == 5 and _seeds_of(resumed, monkeypatch) == want
+    # a group that joins later takes part in the same stream
+    resumed.add_param_group(dict(params=[torch.nn.Parameter(torch.ones(3))]))
+    assert _seeds_of(resumed, monkeypatch) == want + [(5 + 2 * 0x632BE5A7) & 0xFFFFFFFF]
+    # a state that was saved without a seed: the constructor's
+    old = opt.state_dict()
+    for group in old["param_groups"]:
+        group.pop("seed", None)
+    later = make(seed=9)
+    later.load_state_dict(old)
+    assert later.seed == 9 and _seeds_of(later, monkeypatch)[0] == 9
+    later.seed = 11
+    assert _seeds_of(later, monkeypatch)[0] == 11
