@@ -414,7 +414,7 @@ SUBM3D_API subm3d_status subm3d_pool(const subm3d_map* fine, const int32_t* coor
  *   weight, bias  (device) [C] in affine_dtype, each may be NULL (1 and 0).
  *             affine_dtype is SUBM3D_F32 or dtype.
  *   y         (device) [N, C] contiguous, in dtype.  It may be x itself when
- *             x_stride = C; any other overlap is SUBM3D_E_INVALID.
+ *             x_stride = C or N = 1; any other overlap is SUBM3D_E_INVALID.
  *   mean, rstd  (device) fp32 [N], for the backward; both or neither (NULL).
  *   act       SUBM3D_ACT_*; eps >= 0.
  *

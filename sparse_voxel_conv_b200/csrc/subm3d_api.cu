@@ -539,7 +539,7 @@ subm3d_status subm3d_layer_norm(const void* x, int64_t n, int32_t channels, int6
   if (!aligned(x, esz) || !aligned(y, esz) || !aligned(weight, asz) || !aligned(bias, asz) ||
       !aligned(mean, 4) || !aligned(rstd, 4))
     return SUBM3D_E_INVALID;
-  const bool in_place = y == x && x_stride == channels;
+  const bool in_place = y == x && (n == 1 || x_stride == channels);
   Span spans[] = {span(in_place ? nullptr : x, rows_bytes(n, x_stride, channels, esz), false),
                   span(weight, channels * static_cast<int64_t>(asz), false),
                   span(bias, channels * static_cast<int64_t>(asz), false),

@@ -18,12 +18,13 @@ __all__ = ["layer_norm", "layer_norm_forward", "layer_norm_backward", "LayerNorm
 
 
 def _rows(t: torch.Tensor, name: str):
-    """t as rows of its last dimension: (tensor, row stride), a view where it can be."""
+    """t as rows of its last dimension: (tensor, row stride), a view where it can be.  (A
+    single row is contiguous whatever torch gives as its stride.)"""
     shape = t.shape
     if not shape or shape[-1] == 0:
         raise ValueError(f"{name} must have at least one channel")
     c = shape[-1]
-    if len(shape) == 2:
+    if len(shape) == 2 and shape[0] > 1:
         row, col = t.stride()
         if col == 1 and row >= c:
             return t, row

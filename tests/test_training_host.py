@@ -61,3 +61,15 @@ def test_optimizer_keeps_its_seed(S, bits, monkeypatch):
     assert later.seed == 9 and _seeds_of(later, monkeypatch)[0] == 9
     later.seed = 11
     assert _seeds_of(later, monkeypatch)[0] == 11
+
+
+def test_stride_of_a_single_row(S):
+    """A single row's stride says nothing: it is the row's own width to the library."""
+    from sparse_voxel_conv_b200.norm import _rows
+    buf = torch.zeros(4, 131)
+    for x in (buf[:1, :64], buf[3:, 2:66], buf[1:2], buf[:0, :64]):
+        t, stride = _rows(x, "x")
+        assert t is x and (stride == x.shape[1] or not len(x))
+    for x in (buf[:2, :64], buf[1:, 2:66]):
+        t, stride = _rows(x, "x")
+        assert t is x and stride == 131

@@ -6,6 +6,8 @@ import io
 import pytest
 import torch
 
+from tests import train_reference as R
+
 pytestmark = pytest.mark.gpu
 
 BF, F32 = torch.bfloat16, torch.float32
@@ -63,3 +65,27 @@ def test_resumed_optimizer_rounds_alike(S):
         steps(other, (2,))
         assert all(torch.equal(p, q) for p, q in zip(bytes_of(other), want))
     assert not all(torch.equal(p, q) for p, q in zip(bytes_of(plain), want))    # the seed matters
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_norm_of_a_single_row_of_a_wider_matrix(S, dtype):
+    """One row is contiguous whatever its stride: it is normed in place, out of place and
+    backwards like a row that lies alone, and nothing beside it is written."""
+    c, wide = 64, 131
+    buf = torch.randn(3, wide, device="cuda").to(dtype)
+    w, b = torch.rand(c, device="cuda"), torch.rand(c, device="cuda")
+    dy = torch.randn(1, wide, device="cuda").to(dtype)[:, :c]
+    for x in (buf[:1, :c], buf[1:2, 2:c + 2], buf[2:, 64:64 + c]):
+        assert x.stride(0) == wide and x.is_contiguous()
+        ref = R.Norm(x, w, b, 1e-5, "silu")
+        y, mean, rstd = S.layer_norm_forward(x, w, b, act="silu")
+        R.check(y, ref.y, ref.y_bound(), "y")
+        want, bounds = ref.backward(dy)
+        for p, q, e in zip(S.layer_norm_backward(dy, x, mean, rstd, w, b, act="silu"), want, bounds):
+            R.check(p, q, e, "gradient")
+        around = buf.clone()
+        assert S.layer_norm(x, w, b, act="silu", out=x) is x
+        assert torch.equal(x, y)
+        mine = torch.zeros_like(buf, dtype=torch.bool)
+        torch.as_strided(mine, x.shape, x.stride(), x.storage_offset()).fill_(True)
+        assert torch.equal(buf[~mine], around[~mine])
