@@ -163,14 +163,15 @@ def backward_weight(h: MapHandle, feats: torch.Tensor, dy: torch.Tensor, flip: b
 
 
 class _SubMConvFunction(torch.autograd.Function):
-    """out = conv(feats, weight) on a built map, differentiable in feats and
-    weight through the library's backward kernels."""
+    """out = conv(feats, weight) + residual on a built map, differentiable in feats and
+    weight through the library's backward kernels, and in the residual, whose gradient
+    is the output's."""
 
     @staticmethod
-    def forward(ctx, feats, weight, h, flip):
+    def forward(ctx, feats, weight, h, flip, residual):
         ctx.save_for_backward(feats, weight)
         ctx.h, ctx.flip = h, flip
-        return forward(h, feats, weight, flip=flip)
+        return forward(h, feats, weight, flip=flip, residual=residual)
 
     @staticmethod
     def backward(ctx, grad_out):
@@ -182,7 +183,7 @@ class _SubMConvFunction(torch.autograd.Function):
         if ctx.needs_input_grad[1]:
             dw = backward_weight(ctx.h, feats, grad_out, flip=ctx.flip).to(weight.dtype)
             dw = dw.reshape(weight.shape)
-        return dx, dw, None, None
+        return dx, dw, None, None, grad_out if ctx.needs_input_grad[4] else None
 
 
 def run_layout_tensors(h: MapHandle):
@@ -261,10 +262,10 @@ class SubMConv3d(torch.nn.Module):
         wants_grad = torch.is_grad_enabled() and (self.weight.requires_grad or
                                                    x.feats.requires_grad)
         if wants_grad:
-            if self.act is not None or self.bias is not None or residual is not None:
+            if self.act is not None or self.bias is not None:
                 raise NotImplementedError(
-                    "gradients are implemented for the plain convolution (no act, bias, residual)")
-            return x.replace(_SubMConvFunction.apply(x.feats, self.weight, h, self.flip))
+                    "gradients are implemented for the convolution with a residual (no act, bias)")
+            return x.replace(_SubMConvFunction.apply(x.feats, self.weight, h, self.flip, residual))
         y = forward(h, x.feats, self.weight, flip=self.flip, act=self.act, bias=self.bias,
                     residual=residual)
         return x.replace(y)
@@ -286,8 +287,8 @@ class SubMResBlock3d(torch.nn.Module):
         h   = conv1(act(norm1(x)))
         out = conv2(act(norm2(h))) + x
 
-    Without recorded gradients the skip add is conv2's epilogue; with them it is
-    an add of its own, after conv2's output has been rounded.
+    The skip add is conv2's epilogue, with and without recorded gradients (its own
+    gradient is the output's): training and inference give the same bits.
     """
 
     def __init__(self, channels: int, indice_key: str = "subm0", act: str = "silu",
@@ -309,11 +310,10 @@ class SubMResBlock3d(torch.nn.Module):
     def forward(self, x: SparseTensor) -> SparseTensor:
         if self.norm1 is None:
             return self.conv2(self.conv1(x), residual=x.feats)
-        h = self.norm2(self.conv1(self.norm1(x)))
-        if torch.is_grad_enabled() and (h.feats.requires_grad or self.conv2.weight.requires_grad):
-            y = self.conv2(h)
-            return y.replace(y.feats + x.feats)
-        return self.conv2(h, residual=x.feats)
+        skip = x.feats
+        if skip.data_ptr() % 16:    # the norm takes such features, a residual of bf16 may not be
+            skip = skip.clone(memory_format=torch.contiguous_format)
+        return self.conv2(self.norm2(self.conv1(self.norm1(x))), residual=skip)
 
 
 # ------------------------------------------------------ resolution changes ----

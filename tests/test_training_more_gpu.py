@@ -6,6 +6,7 @@ import io
 import pytest
 import torch
 
+import workloads as WL
 from tests import train_reference as R
 
 pytestmark = pytest.mark.gpu
@@ -89,3 +90,36 @@ def test_norm_of_a_single_row_of_a_wider_matrix(S, dtype):
         mine = torch.zeros_like(buf, dtype=torch.bool)
         torch.as_strided(mine, x.shape, x.stride(), x.storage_offset()).fill_(True)
         assert torch.equal(buf[~mine], around[~mine])
+
+
+@pytest.mark.parametrize("dtype,c,key", [(BF, 64, "shell"), (BF, 32, "shell"), (F32, 24, "shell")])
+def test_block_is_one_function(S, dtype, c, key):
+    """SubMResBlock3d(norm=True) gives the same bits with and without recorded gradients, also
+    for features that start between 16-byte borders; the skip's gradient is the output's."""
+    wl = WL.make_workload(key)
+    coords = torch.from_numpy(wl.coords).cuda()
+    n = coords.shape[0]
+    torch.manual_seed(3)
+    block = S.SubMResBlock3d(c, dtype=dtype, device="cuda", norm=True)
+    buf = torch.randn(n * c + 1, device="cuda").to(dtype)
+    cache = {}
+    for x in (buf[:-1].view(n, c), buf[1:].view(n, c), buf[:n // 2 * 2 * c].view(n // 2, 2 * c)[:, :c]):
+        st = S.SparseTensor(coords[:x.shape[0]], x, wl.grid_dim, wl.batch, cache if x.shape[0] == n else None)
+        with torch.no_grad():
+            want = block(st).feats
+        for p in block.parameters():
+            p.requires_grad_(True)
+        leaf = x.detach().requires_grad_(True)      # where x lies: the norm sums in the order of its borders
+        y = block(st.replace(x)).feats
+        assert y.requires_grad and torch.equal(y.detach(), want)
+        y = block(st.replace(leaf)).feats
+        assert torch.equal(y.detach(), want)
+        dy = torch.randn_like(want)
+        dx, = torch.autograd.grad(y, leaf, dy)
+        # conv2's own output without the skip has the gradient dx - dy
+        h = block.norm2(block.conv1(block.norm1(st.replace(leaf))))
+        inner, = torch.autograd.grad(block.conv2(h).feats, leaf, dy)
+        half = torch.finfo(dtype).eps / 2
+        assert ((dx.double() - inner.double() - dy.double()).abs() <= half * dx.double().abs() * 1.01).all()
+        for p in block.parameters():
+            p.requires_grad_(False)
