@@ -3,6 +3,7 @@ tensor argument, and the rules for calls on another stream or device."""
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _abi
 
@@ -70,3 +71,11 @@ def _written(tensors) -> None:
     """Tells autograd that the library wrote these tensors in place, so that a
     backward pass that had saved one of them fails instead of using the new values."""
     torch.autograd.graph.increment_version(tensors)
+
+
+def _no_tangents(*tensors) -> None:
+    """Refuses forward-mode tangents: the library's calls would drop them."""
+    if forward_ad._current_level < 0:
+        return
+    if any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise NotImplementedError("forward-mode derivatives are not implemented")

@@ -11,8 +11,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _abi
-from ._host import _ACTS, _DTYPES, _current_device, _device_of, _new, _on_side_stream, \
-    _same_device, _written
+from ._host import _ACTS, _DTYPES, _current_device, _device_of, _new, _no_tangents, \
+    _on_side_stream, _same_device, _written
 
 __all__ = ["layer_norm", "layer_norm_forward", "layer_norm_backward", "LayerNorm"]
 
@@ -98,7 +98,7 @@ def layer_norm_forward(x: torch.Tensor, weight: torch.Tensor | None = None,
                        bias: torch.Tensor | None = None, eps: float = 1e-5,
                        act: str | None = None, out: torch.Tensor | None = None, stream=None):
     """(y, mean, rstd): layer_norm() and the row statistics (fp32 [rows]) that
-    layer_norm_backward() takes."""
+    layer_norm_backward() takes.  Neither of these two is recorded by autograd."""
     return _norm(x, weight, bias, eps, act, out, stream, True)
 
 
@@ -190,9 +190,10 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
     x: [..., C] float32 or bfloat16 (rows of a matrix may be strided); weight, bias:
     optional [C], float32 or x's dtype.  act: None, "gelu" (exact erf form) or
     "silu".  fp32 arithmetic; y has x's dtype and is rounded once.  Differentiable
-    in x, weight and bias; out (contiguous, may be x) and stream are for calls that
-    autograd does not record.
+    in x, weight and bias (forward-mode tangents are refused); out (contiguous, may be
+    x) and stream are for calls that autograd does not record.
     """
+    _no_tangents(x, weight, bias)
     if torch.is_grad_enabled() and (x.requires_grad or
                                     (weight is not None and weight.requires_grad) or
                                     (bias is not None and bias.requires_grad)):

@@ -11,8 +11,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _abi
-from ._host import _DTYPES, _current_device, _device_of, _new, _on_side_stream, _same_device, \
-    _written
+from ._host import _DTYPES, _current_device, _device_of, _new, _no_tangents, _on_side_stream, \
+    _same_device, _written
 
 __all__ = ["rotary", "VoxelRotary"]
 
@@ -102,9 +102,10 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, theta: float = 10000.0, axi
     pairs turn with each axis, in order (default: an equal share each); the rest is
     copied.  Pair j of an axis with n pairs turns by position * theta ** (-j / n).
     interleaved: pairs are (2p, 2p + 1), else (p, p + head_dim / 2).  inverse turns
-    back.  out may be x (in place).  Differentiable in x; out and stream are for
-    calls that autograd does not record.
+    back.  out may be x (in place).  Differentiable in x (forward-mode tangents are
+    refused); out and stream are for calls that autograd does not record.
     """
+    _no_tangents(x, positions)
     if torch.is_grad_enabled() and x.requires_grad:
         if out is not None or stream is not None:
             raise ValueError("out and stream are not available where gradients are recorded")

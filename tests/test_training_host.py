@@ -73,3 +73,25 @@ def test_stride_of_a_single_row(S):
     for x in (buf[:2, :64], buf[1:, 2:66]):
         t, stride = _rows(x, "x")
         assert t is x and stride == 131
+
+
+def test_tangents_are_refused(S):
+    """Forward-mode tangents, which no kernel carries on, are not dropped without a word."""
+    from torch.autograd import forward_ad
+    x, w, b = torch.randn(4, 16), torch.ones(16), torch.zeros(16)
+    pos, where = torch.zeros(4, 3, dtype=torch.int32), torch.zeros(4, 3)
+    with forward_ad.dual_level():
+        dual = lambda t: forward_ad.make_dual(t, torch.ones_like(t))  # noqa: E731
+        for call in (lambda: S.layer_norm(dual(x)), lambda: S.layer_norm(x, dual(w), b),
+                     lambda: S.layer_norm(x, w, dual(b)), lambda: S.LayerNorm(16)(dual(x)),
+                     lambda: S.rotary(dual(x), pos), lambda: S.rotary(x, dual(where))):
+            with pytest.raises(NotImplementedError, match="forward-mode"):
+                call()
+            with torch.no_grad(), pytest.raises(NotImplementedError, match="forward-mode"):
+                call()
+        for call in (lambda: S.layer_norm(x, w, b), lambda: S.rotary(x, pos)):  # nothing to drop
+            with pytest.raises(ValueError, match="CUDA"):
+                call()
+    for f in (lambda t: S.layer_norm(t, w, b), lambda t: S.rotary(t, pos)):
+        with pytest.raises(NotImplementedError, match="forward-mode"):
+            torch.func.jvp(f, (x,), (torch.ones_like(x),))
