@@ -79,3 +79,10 @@ def _no_tangents(*tensors) -> None:
         return
     if any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
         raise NotImplementedError("forward-mode derivatives are not implemented")
+
+
+def _writable(out) -> None:
+    """Refuses an `out` that autograd records: its gradient would go on as if the library had
+    written nothing."""
+    if out.requires_grad and torch.is_grad_enabled():
+        raise ValueError("out is a recorded tensor (requires_grad): detach it, or call in no_grad()")

@@ -12,7 +12,7 @@ from torch.autograd.function import once_differentiable
 
 from . import _abi
 from ._host import _ACTS, _DTYPES, _current_device, _device_of, _new, _no_tangents, \
-    _on_side_stream, _same_device, _written
+    _on_side_stream, _same_device, _writable, _written
 
 __all__ = ["layer_norm", "layer_norm_forward", "layer_norm_backward", "LayerNorm"]
 
@@ -61,6 +61,8 @@ def _codes(dtype, act):
 
 
 def _norm(x, weight, bias, eps, act, out, stream, stats: bool):
+    if out is not None:
+        _writable(out)
     dev = x.get_device()
     if dev < 0 or dev != _current_device():
         with torch.cuda.device(_device_of(x, "x")):

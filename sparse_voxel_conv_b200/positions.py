@@ -12,12 +12,14 @@ from torch.autograd.function import once_differentiable
 
 from . import _abi
 from ._host import _DTYPES, _current_device, _device_of, _new, _no_tangents, _on_side_stream, \
-    _same_device, _written
+    _same_device, _writable, _written
 
 __all__ = ["rotary", "VoxelRotary"]
 
 
 def _turn(x, positions, theta, axis_pairs, interleaved, inverse, out, stream):
+    if out is not None:
+        _writable(out)
     dev = x.get_device()
     if dev < 0 or dev != _current_device():
         with torch.cuda.device(_device_of(x, "x")):

@@ -95,3 +95,17 @@ def test_tangents_are_refused(S):
     for f in (lambda t: S.layer_norm(t, w, b), lambda t: S.rotary(t, pos)):
         with pytest.raises(NotImplementedError, match="forward-mode"):
             torch.func.jvp(f, (x,), (torch.ones_like(x),))
+
+
+def test_recorded_outputs_are_refused(S):
+    """out= may not be a tensor of a recorded graph, whose gradient would go on as if nothing
+    had been written; without recording it may."""
+    x, pos = torch.randn(4, 16), torch.zeros(4, 3, dtype=torch.int32)
+    leaf = torch.zeros(4, 16, requires_grad=True)
+    for out in (leaf, leaf * 1):
+        for call in (lambda: S.layer_norm(x, out=out), lambda: S.layer_norm_forward(x, out=out),
+                     lambda: S.rotary(x, pos, out=out)):
+            with pytest.raises(ValueError, match="recorded"):
+                call()
+            with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):      # as far as the CPU goes
+                call()
