@@ -104,11 +104,14 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, theta: float = 10000.0, axi
     pairs turn with each axis, in order (default: an equal share each); the rest is
     copied.  Pair j of an axis with n pairs turns by position * theta ** (-j / n).
     interleaved: pairs are (2p, 2p + 1), else (p, p + head_dim / 2).  inverse turns
-    back.  out may be x (in place).  Differentiable in x (forward-mode tangents are
-    refused); out and stream are for calls that autograd does not record.
+    back.  out may be x (in place).  Differentiable in x, not in the positions, which
+    may not require a gradient (forward-mode tangents are refused too); out and stream
+    are for calls that autograd does not record.
     """
     _no_tangents(x, positions)
-    if torch.is_grad_enabled() and x.requires_grad:
+    if torch.is_grad_enabled() and (x.requires_grad or positions.requires_grad):
+        if positions.requires_grad:
+            raise ValueError("positions have no gradient: detach them")
         if out is not None or stream is not None:
             raise ValueError("out and stream are not available where gradients are recorded")
         return _RotaryFunction.apply(x, positions, theta, axis_pairs, interleaved, inverse)

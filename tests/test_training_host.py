@@ -109,3 +109,14 @@ def test_recorded_outputs_are_refused(S):
                 call()
             with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):      # as far as the CPU goes
                 call()
+
+
+def test_positions_have_no_gradient(S):
+    """Positions that ask for a gradient are refused where one would be recorded."""
+    x, where = torch.randn(4, 16), torch.zeros(4, 3, requires_grad=True)
+    for t in (x, x.clone().requires_grad_(True)):
+        with pytest.raises(ValueError, match="positions have no gradient"):
+            S.rotary(t, where)
+        for quiet in (where.detach(), where):
+            with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):      # as far as the CPU goes
+                S.rotary(t, quiet)
