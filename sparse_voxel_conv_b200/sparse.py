@@ -308,7 +308,7 @@ class SubMResBlock3d(torch.nn.Module):
                                 device=device, bias=True)
 
     def forward(self, x: SparseTensor) -> SparseTensor:
-        if self.norm1 is None:
+        if getattr(self, "norm1", None) is None:    # (a block from an older file has no such name)
             return self.conv2(self.conv1(x), residual=x.feats)
         skip = x.feats
         if skip.data_ptr() % 16:    # the norm takes such features, a residual of bf16 may not be

@@ -120,3 +120,14 @@ def test_positions_have_no_gradient(S):
         for quiet in (where.detach(), where):
             with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):      # as far as the CPU goes
                 S.rotary(t, quiet)
+
+
+def test_block_that_was_saved_whole_before_it_had_norms(S):
+    """A SubMResBlock3d object from a file that knows no norms runs as the block without them."""
+    block = S.SubMResBlock3d(16, dtype=torch.float32)
+    old = copy.deepcopy(block)
+    del old.__dict__["norm1"]
+    x = S.SparseTensor(torch.zeros(1, 4, dtype=torch.int32), torch.zeros(1, 16), 4)
+    for b in (block, old, _through_file(old)):
+        with pytest.raises(ValueError, match="CUDA"):       # as far as the CPU goes
+            b(x)
