@@ -85,4 +85,4 @@ def _writable(out) -> None:
     """Refuses an `out` that autograd records: its gradient would go on as if the library had
     written nothing."""
     if out.requires_grad and torch.is_grad_enabled():
-        raise ValueError("out is a recorded tensor (requires_grad): detach it, or call in no_grad()")
+        raise ValueError("out is a recorded tensor (requires_grad): detach it or use no_grad()")

@@ -123,3 +123,78 @@ def test_block_is_one_function(S, dtype, c, key):
         assert ((dx.double() - inner.double() - dy.double()).abs() <= half * dx.double().abs() * 1.01).all()
         for p in block.parameters():
             p.requires_grad_(False)
+
+
+def _differences(forward, backward, x, dy, w, b, act):
+    """[(name, difference quotient, <gradient, direction>, slack, the same product for gradients
+    with a fault)] of f = <dy, y> in directions of x, w and b.
+
+    forward(x, w, b) -> y and backward(x, w, b) -> (dx, dw, db) in fp32.  The quotient over
+    +-h differs from the slope by the cubic term, told from the formula's own quotients at h
+    and h / 2 in 64 bits (their difference is 3/4 of it), by what y's rounding puts into f, at
+    most <|dy|, bound of y> on each side over 2 h, and by the gradient's own bound."""
+    ref = R.Norm(x, w, b, 1e-5, act)
+    (dx, dw, db), bounds = ref.backward(dy)
+    dz = dy.double() * R.act_slope(ref.z, act)
+    g = dz * ref.w
+    mean0, mean1 = g.mean(1, keepdim=True), (g * ref.xhat).mean(1, keepdim=True)
+    # directions that each of the gradient's terms reaches: along the rows' own shift and
+    # scale (where y stands still and the two means have to cancel g), and any other
+    r = torch.Generator(device="cpu")
+    r.manual_seed(x.shape[1])
+    v = torch.randn(x.shape, generator=r, dtype=torch.float64).to(x.device) + mean0.sign() + mean1.sign() * ref.xhat
+    v = v + (ref.rstd * g).sign()
+    faults = {
+        "x": dict(nothing=0 * dx, sign=-dx, mean=dx + ref.rstd * mean0, slope=dx + ref.rstd * ref.xhat * mean1,
+                  both=ref.rstd * g),
+        "w": dict(nothing=0 * dw, sign=-dw, unnormed=(dz * x.double()).sum(0)),
+        "b": dict(nothing=0 * db, sign=-db),
+    }
+    if act:     # the activation's slope forgotten
+        faults["w"]["act"] = (dy.double() * ref.xhat).sum(0)
+        faults["b"]["act"] = dy.double().sum(0)
+    got = dict(zip("xwb", backward(x, w, b)))
+    at = dict(x=x, w=w, b=b)
+    out = []
+    for name, bound in zip("xwb", bounds):
+        d = v if name == "x" else dict(w=dw, b=db)[name].sign() * (0.5 + torch.rand(
+            w.shape, generator=r, dtype=torch.float64).to(x.device))
+
+        def quotient(h, kernel):
+            """(quotient, its direction, the rounding's share); both sides are fp32 numbers."""
+            sides = [{**at, name: (at[name].double() + s * h * d).float()} for s in (1, -1)]
+            refs = [R.Norm(a["x"], a["w"], a["b"], 1e-5, act) for a in sides]
+            ys = [forward(a["x"], a["w"], a["b"]).double() if kernel else n.y for a, n in zip(sides, refs)]
+            f = [(dy.double() * y).sum().item() for y in ys]
+            noise = sum((dy.double().abs() * n.y_bound()).sum().item() for n in refs)
+            way = (sides[0][name].double() - sides[1][name].double()) / (2 * h)
+            return (f[0] - f[1]) / (2 * h), way, noise / (2 * h)
+
+        h = 2.0 ** -6
+        num, way, noise = quotient(h, True)
+        cubic = abs(quotient(h, False)[0] - quotient(h / 2, False)[0]) * 4 / 3
+        slack = 2 * cubic + noise + (bound * way.abs()).sum().item()
+        out.append((name, num, (got[name].double() * way).sum().item(), slack,
+                    {k: (q * way).sum().item() for k, q in faults[name].items()}))
+    return out
+
+
+@pytest.mark.parametrize("n,c", [(64, 48), (64, 75), (24, 1536), (12, 8200)])
+@pytest.mark.parametrize("act", [None, "gelu", "silu"])
+def test_norm_gradient_against_differences(S, n, c, act):
+    """fp32: the gradient is the slope that the forward's differences show, and a gradient with
+    a term left out, a wrong sign or without the activation's slope is not."""
+    g = torch.Generator(device="cpu")
+    g.manual_seed(n + c + 1)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    x, dy, w, b = r(n, c) + 0.3 * r(c), r(n, c) + 0.3, 1 + 0.3 * r(c), 0.3 * r(c)
+    x, dy, w, b = (t.cuda() for t in (x, dy, w, b))
+
+    def backward(x, w, b):
+        _, mean, rstd = S.layer_norm_forward(x, w, b, act=act)
+        return S.layer_norm_backward(dy, x, mean, rstd, w, b, act=act)
+
+    for name, num, ana, slack, faults in _differences(lambda *a: S.layer_norm(*a, act=act), backward, x, dy, w, b, act):
+        assert abs(num - ana) <= slack, (name, num, ana, slack)
+        for what, wrong in faults.items():
+            assert abs(num - wrong) > 2 * slack, (name, what, num, wrong, slack)
