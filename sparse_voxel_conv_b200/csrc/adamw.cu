@@ -1,4 +1,4 @@
-// One AdamW step over many tensors in one launch.
+// One AdamW step over a list of tensors, up to kAdamWMany of them in a launch.
 //
 //   m' = b1 m + (1 - b1) g,  v' = b2 v + (1 - b2) g^2,
 //   p' = p (1 - lr wd) - lr / (1 - b1^t) * m' / (sqrt(v') / sqrt(1 - b2^t) + eps).
@@ -18,13 +18,16 @@
 // gets the scale 255 (NaN): all its 32 elements are NaN from then on.
 //
 // Bound by HBM: 28 bytes an element with fp32 weights and 32-bit moments (28.3 M
-// elements 119 us, 6.65 TB/s, the copy rate), 18.1 with bf16 weights, fp32 gradients
-// and masters and 8-bit moments (56.6 M elements 158 us at full clock, 6.5 TB/s; 172
+// elements 116 us, 6.8 TB/s, the copy rate), 18.1 with bf16 weights, fp32 gradients
+// and masters and 8-bit moments (56.6 M elements 161 us at full clock, 6.4 TB/s; 176
 // in a sustained run, whose power lowers the clock: its 67 instructions an element
 // count).  A thread takes 8 consecutive elements: 16-byte accesses, and a block of 32
 // elements is four lanes', whose largest magnitude two shuffles find.  Arithmetic on
 // pairs (f32x2).  Four blocks of 256 threads an SM: with five or six the registers
 // spill (178 us), with two groups of elements a thread fewer loads overlap (195).
+// These are with the host's step and rate.  With the device's (hyper_of) every thread
+// forms the factors in fp64: 119 us for the first case, 219 us for the second, which
+// the instructions bound.
 //
 // The moments' products and sums are rounded one by one (no fma), so that the
 // states are the same bits as the formula in elementary fp32 operations gives.
@@ -243,8 +246,9 @@ __device__ __forceinline__ float rcp_fast(float v) {
 // The correctly rounded roots of a pair of numbers in [2^-100, 2^127): an estimate of
 // 1 / sqrt(v), then one step on the root with the remainder v - g^2 formed exactly by an
 // fma (Markstein, Computation of elementary functions on the IBM RISC System/6000
-// processor, IBM J. Res. Dev. 34, 1990).  Compared with sqrt.rn for every number of that
-// range.  On pairs it takes half the instructions of two sqrt.rn and no branch.
+// processor, IBM J. Res. Dev. 34, 1990).  All 1,904,214,016
+// numbers of that range gave sqrt.rn's bits on a B200.  On pairs it takes half the
+// instructions of two sqrt.rn and no branch.
 constexpr uint32_t kRootFirst = (127u - 100u) << 23, kRootCount = 227u << 23;
 __device__ __forceinline__ f2 root_pair(f2 v) {
   float a, b;

@@ -14,8 +14,8 @@
 // row read again from the caches for every pass.
 //
 // Both directions are bound by HBM where there is no activation (329,839 x 128 bf16:
-// forward 28.9 us, 5.8 TB/s; backward 43.7 us, 5.8 TB/s).  SiLU adds two instructions
-// of the special-function pipe an element (19 us of it): 31 us and 46 us in a
+// forward 29.3 us, 5.8 TB/s; backward 43.4 us, 5.8 TB/s).  SiLU adds two instructions
+// of the special-function pipe an element (19 us of it): 32 us and 48 us in a
 // sustained run.  The steps from 568 and 913 us: one read by a block a row -> rows in
 // registers of small teams (36 / 90) -> rows ahead by cp.async, pairs (30 / 63) ->
 // no recomputed addresses and no branches in the copies (30 / 47) -> one block an SM
@@ -350,7 +350,10 @@ __device__ __forceinline__ f2 sigmoid_pair(f2 z) {
 }
 
 // Phi(z) and exp(-z^2 / 2) of a pair: the rational-times-Gaussian form that
-// gelu_erf uses (epilogue.cuh), with the factor 1/2 of Phi in its coefficients.
+// gelu_erf uses (epilogue.cuh: Abramowitz & Stegun, eq. 7.1.26, erfc off by at most
+// 1.5e-7), with the factor 1/2 of Phi in its coefficients.  With its fp32 roundings Phi
+// is off by up to 5 units of 2^-24 (an erf in fp32: 1); the convolution's
+// epilogue and this norm give one GELU.
 __device__ __forceinline__ f2 phi_pair(f2 z, f2& gauss) {
   const f2 mag = z & 0x7FFFFFFF7FFFFFFFull;
   const f2 t = rcp_pair(f2_fma(mag, f2_set(0.3275911f * 0.70710678118654752f), f2_set(1.0f)));

@@ -18,7 +18,7 @@
 // alignment allows up to 16 bytes (two loads half a vector apart in the halves
 // layout), computes their cos and sin once, while its first loads are on their way,
 // and keeps them in registers over a run of the row's heads.  With a head or two a
-// row the angles bound it instead (131,072 x 1 x 64 bf16: 21 us).
+// row the angles bound it instead (131,072 x 1 x 64 bf16: 22 us, its bytes 5.4).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

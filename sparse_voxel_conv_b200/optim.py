@@ -1,7 +1,8 @@
-"""AdamW over many tensors in one launch, with moments in 32 or in 8 bits.
+"""AdamW over lists of tensors, with moments in 32 or in 8 bits.
 
 What a training loop does with the gradients of backward_weight() and of the
-autograd functions: one call of libsubm3d.so updates all weights and moments.
+autograd functions: one call of libsubm3d.so updates the weights and moments of all
+tensors of one set of types, up to 400 of them in one launch.
 """
 from __future__ import annotations
 
