@@ -236,7 +236,8 @@ class SubMConv3d(torch.nn.Module):
     indice_key reuse one neighbour map per SparseTensor coordinate set.
     flip selects the mirrored kernel; act=None, "gelu" (exact erf form) or
     "silu".  bias=True adds a [Cout] bias before the activation (the pages'
-    op has none; the residual blocks' convolutions do).
+    op has none; the residual blocks' convolutions do).  Differentiable, the
+    residual of a call included, without an activation and a bias.
     """
 
     def __init__(self, in_channels: int, out_channels: int, indice_key: str = "subm0",
@@ -259,10 +260,12 @@ class SubMConv3d(torch.nn.Module):
 
     def forward(self, x: SparseTensor, residual: torch.Tensor | None = None) -> SparseTensor:
         h = x.get_map(self.indice_key)
-        wants_grad = torch.is_grad_enabled() and (self.weight.requires_grad or
-                                                   x.feats.requires_grad)
+        plain = self.act is None and self.bias is None
+        wants_grad = torch.is_grad_enabled() and (
+            self.weight.requires_grad or x.feats.requires_grad or
+            (plain and residual is not None and residual.requires_grad))
         if wants_grad:
-            if self.act is not None or self.bias is not None:
+            if not plain:
                 raise NotImplementedError(
                     "gradients are implemented for the convolution with a residual (no act, bias)")
             return x.replace(_SubMConvFunction.apply(x.feats, self.weight, h, self.flip, residual))

@@ -198,3 +198,20 @@ def test_norm_gradient_against_differences(S, n, c, act):
         assert abs(num - ana) <= slack, (name, num, ana, slack)
         for what, wrong in faults.items():
             assert abs(num - wrong) > 2 * slack, (name, what, num, wrong, slack)
+
+
+def test_residual_alone_has_its_gradient(S):
+    """A frozen convolution of features without a gradient hands the residual's on."""
+    wl = WL.make_workload("shell")
+    coords = torch.from_numpy(wl.coords).cuda()
+    n, c = coords.shape[0], 32
+    conv = S.SubMConv3d(c, c, device="cuda")
+    st = S.SparseTensor(coords, torch.randn(n, c, device="cuda").to(BF), wl.grid_dim, wl.batch)
+    residual = torch.randn(n, c, device="cuda").to(BF)
+    want = conv(st, residual=residual).feats
+    assert not want.requires_grad
+    leaf = residual.clone().requires_grad_(True)
+    y = conv(st, residual=leaf).feats
+    dy = torch.randn_like(want)
+    y.backward(dy)
+    assert torch.equal(y.detach(), want) and torch.equal(leaf.grad, dy)
